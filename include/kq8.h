@@ -19,7 +19,8 @@
  *     nothing and keeps no state between calls.
  *   - Calls enqueue work on `stream` (a cudaStream_t; NULL = the legacy default
  *     stream) and return without waiting for it.  Stream order holds as for
- *     ordinary launches.  The decode kernels and the appends are programmatic
+ *     ordinary launches.  The decode kernels, the tree attention and the calls
+ *     that write, read or move cache rows are programmatic
  *     launches (cudaLaunchAttributeProgrammaticStreamSerialization): one of
  *     them may be scheduled while the kernel just before it on the stream
  *     finishes (this library's, or any code's that signals its dependents
@@ -56,6 +57,13 @@ enum {
     KQ8_ERR_UNSUPPORTED = -2, /* shape outside what the kernels implement   */
     KQ8_ERR_WORKSPACE = -3,   /* workspace missing, misaligned or too small  */
     KQ8_ERR_CUDA = -4         /* a CUDA runtime call or launch failed        */
+};
+
+/* Element types of the calls that take one. */
+enum {
+    KQ8_F32 = 0,
+    KQ8_F16 = 1,
+    KQ8_BF16 = 2
 };
 
 /* Status bits written by kernels into the status word. */
@@ -383,6 +391,96 @@ int kq8_decode_attn_q4(float* out, const float* q, const kq8_cache_t* cache,
                        const int32_t* page_table, int32_t max_pages, const int32_t* seq_lens,
                        int32_t max_seq_len, int32_t B, int32_t nq, float scale, void* workspace,
                        size_t workspace_bytes, kq8_stream_t stream);
+
+/*
+ * Cache rows in and out, for the tensors a model holds: fp32, fp16 or bf16
+ * rows of any stride (a slice of a fused QKV projection, a head-major tensor).
+ * Element i of KV head h of token t of K is k[t * k_token_stride + h *
+ * k_head_stride + i], strides in elements, likewise V; the 128 elements of a row
+ * are adjacent.  bits is 8 or 4: the format of the cache (kq8_append_kv,
+ * kq8_append_kv_q4).
+ *   kq8_write_kv : the write path on each row widened to fp32, so codes and
+ *                  maxima equal kq8_append_kv's (kq8_append_kv_q4's) of the same
+ *                  values bit for bit.
+ *   kq8_read_kv  : the values the rows stand for, code * (stored max * (1/127))
+ *                  (q4: 1/7) as one fp32 product, rounded once to dtype.  The rows
+ *                  stored must not overlap (KQ8_ERR_INVALID_ARG).
+ *   dtype  : KQ8_F32, KQ8_F16 or KQ8_BF16, of k and v both; pointers aligned to
+ *            an element (16-byte aligned rows are copied 16 bytes at a time).
+ *   slot, status : as kq8_append_kv.  A token with a negative or bad slot is
+ *            skipped: its row of the cache (write) or of k and v (read) stays as
+ *            it was.  A write's slots must be distinct: of two tokens with one
+ *            slot the cache keeps pieces of either.
+ */
+int kq8_write_kv(const kq8_cache_t* cache, int32_t bits, const void* k, const void* v,
+                 int32_t dtype, size_t k_token_stride, size_t k_head_stride,
+                 size_t v_token_stride, size_t v_head_stride, const int32_t* slot, int32_t T,
+                 uint32_t* status, kq8_stream_t stream);
+int kq8_read_kv(const kq8_cache_t* cache, int32_t bits, void* k, void* v, int32_t dtype,
+                size_t k_token_stride, size_t k_head_stride, size_t v_token_stride,
+                size_t v_head_stride, const int32_t* slot, int32_t T, uint32_t* status,
+                kq8_stream_t stream);
+
+/*
+ * Attention for trees of drafted tokens over the q8 cache (speculative decoding's
+ * verify step).  Sequence b's nb_b = q_offsets[b+1] - q_offsets[b] drafts (the
+ * tree's nodes) are the last nb_b of its seq_lens[b] cached tokens: node i sits at
+ * position seq_lens[b] - nb_b + i (write them with kq8_write_kv first).  Node i
+ * attends the committed tokens 0 .. seq_lens[b] - nb_b - 1 and the nodes j whose
+ * bit is set in its mask row; each is computed as one kq8_decode_attn query over
+ * those tokens (the same Q quantisation, scores and softmax), to fp32 rounding.
+ *   out, q      : dtype [total_q][nq][128], packed by sequence; q with strides of
+ *                 its tokens and heads in elements (multiples of 4), out
+ *                 contiguous; both aligned to 4 elements.  Rows outside every
+ *                 sequence stay as they were.
+ *   dtype       : KQ8_F32, KQ8_F16 or KQ8_BF16, of q and out; outputs are rounded
+ *                 once.  For bf16 the softmax weights enter the value product as
+ *                 fp16 (11 bits), for the others as fp16 hi + lo (22 bits).
+ *   tree_mask   : uint32 [total_q][mask_words]; bit j % 32 of word j / 32 of a node's
+ *                 row: it attends node j (its own bit included).  mask_words * 32 >=
+ *                 max_q_len; bits at and past nb_b are ignored.  A node that attends
+ *                 nothing (no committed token, no bit) gets 0.  NULL: a chain, node
+ *                 i attends nodes 0 .. i.
+ *   max_seq_len, max_q_len : host bounds on seq_lens[b] and nb_b; max_q_len <=
+ *                 KQ8_TREE_MAX_NODES.
+ *   nq          : nq % nkv == 0, G = nq / nkv in 1..8.
+ *   workspace   : kq8_tree_workspace_bytes(...) bytes, 256-byte aligned,
+ *                 initialised once by kq8_workspace_init; calls that share it must
+ *                 not overlap on the GPU.
+ * Bad sequences and pages as kq8_prefill_attn.
+ */
+#define KQ8_TREE_MAX_NODES 1024
+size_t kq8_tree_workspace_bytes(int32_t B, int32_t nq, int32_t nkv, int32_t max_seq_len,
+                                int32_t max_q_len);
+int kq8_tree_attn(void* out, const void* q, int32_t dtype, size_t q_token_stride,
+                  size_t q_head_stride, int32_t total_q, const kq8_cache_t* cache,
+                  const int32_t* page_table, int32_t max_pages, const int32_t* seq_lens,
+                  const int32_t* q_offsets, const uint32_t* tree_mask, int32_t mask_words,
+                  int32_t max_seq_len, int32_t max_q_len, int32_t B, int32_t nq, float scale,
+                  void* workspace, size_t workspace_bytes, kq8_stream_t stream);
+
+/*
+ * The accepted path of a tree moves to its place: for every sequence b and i <
+ * path_len[b], the cache row (codes and maxima, every KV head) at position
+ * base_lens[b] + path[b][i] is copied to position base_lens[b] + i, as if all rows
+ * were read before any is written.  Afterwards the sequence holds base_lens[b] +
+ * path_len[b] tokens; what the positions behind them hold is unspecified.
+ *   bits      : 8 or 4, the format of the cache.
+ *   base_lens : int32 [B] (device): committed tokens, seq_lens[b] - nb_b of the
+ *               kq8_tree_attn call.
+ *   path      : int32 [B][max_path] (device): accepted nodes, strictly ascending (a
+ *               node follows its parent); entries from path_len[b] on are ignored.
+ *   path_len  : int32 [B] (device), each in [0, max_path].
+ *   status    : optional uint32 word (device).  A path that does not ascend, a bad
+ *               length or a position outside the page table's row sets
+ *               KQ8_STATUS_BAD_SEQLEN, a bad page id KQ8_STATUS_BAD_PAGE, and that
+ *               sequence moves nothing.
+ * The pages of the moved rows must belong to one sequence only.
+ */
+int kq8_tree_commit(const kq8_cache_t* cache, int32_t bits, const int32_t* page_table,
+                    int32_t max_pages, const int32_t* base_lens, const int32_t* path,
+                    const int32_t* path_len, int32_t max_path, int32_t B, uint32_t* status,
+                    kq8_stream_t stream);
 
 /*
  * Copies the status word of `workspace` (or of a kq8_append_kv status word) to

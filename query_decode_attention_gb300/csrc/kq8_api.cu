@@ -15,6 +15,66 @@ namespace kq8 {
 
 size_t attn_smem_bytes(int G);
 
+// SMs of the current device; without one (plans asked for on a host without a
+// GPU) a GB300's 152.
+int device_sms() {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 152;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
+        return 152;
+    return sms;
+}
+
+// cuTensorMapEncodeTiled, looked up once through the runtime (no link to the
+// driver library).
+static PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                             &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    });
+    return fn;
+}
+
+int encode_tensor_map(CUtensorMap* map, CUtensorMapDataType type, uint32_t rank, void* base,
+                      const uint64_t* dims, const uint64_t* strides, const uint32_t* box,
+                      CUtensorMapSwizzle swizzle) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc || rank > 5) return KQ8_ERR_CUDA;
+    cuuint64_t d[5], st[5];
+    cuuint32_t bx[5], estr[5];
+    for (uint32_t i = 0; i < rank; i++) {
+        d[i] = dims[i];
+        if (i + 1 < rank) st[i] = strides[i];
+        bx[i] = box[i];
+        estr[i] = 1u;
+    }
+    const CUresult r = enc(map, type, rank, base, d, st, bx, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? KQ8_OK : KQ8_ERR_CUDA;
+}
+
+// The V array as the 3-D tensor the attention kernels copy sub-tiles of:
+// {row bytes, kv_bs rows, num_pages * nkv (page, head) pairs}, boxes of 32 rows.
+// q8 rows are 128 bytes (128-byte swizzle in shared memory), q4 rows 64 bytes
+// (64-byte swizzle).
+int encode_vmap(CUtensorMap* map, const kq8_cache_t& c, bool q4) {
+    const uint64_t pairs = (uint64_t)c.num_pages * (uint64_t)c.num_kv_heads;
+    if (pairs > 0x7FFFFFFFull) return KQ8_ERR_UNSUPPORTED;  // the copy's coordinate is int32
+    const uint64_t row = q4 ? HD / 2 : HD;
+    const uint64_t dims[3] = {row, (uint64_t)c.kv_bs, pairs};
+    const uint64_t strides[2] = {row, (uint64_t)c.kv_bs * row};
+    const uint32_t box[3] = {(uint32_t)row, (uint32_t)TILE, 1u};
+    return encode_tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, c.v, dims, strides, box,
+                             q4 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
 namespace {
 
 constexpr size_t WS_ALIGN = 256;
@@ -28,16 +88,6 @@ constexpr size_t HEADER_BYTES = STATUS_BYTES + MAX_COUNTERS * sizeof(uint32_t);
 
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
-
-// SMs of the current device; without one (plans asked for on a host without a
-// GPU) a GB300's 152.
-int device_sms() {
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 152;
-    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
-        return 152;
-    return sms;
-}
 
 #ifndef KQ8_MAX_CHUNK
 #define KQ8_MAX_CHUNK 128
@@ -219,44 +269,6 @@ AttnParams attn_params(float* out, const float* q, const kq8_cache_t* c, const i
     return p;
 }
 
-// cuTensorMapEncodeTiled, looked up once through the runtime (no link to the
-// driver library).
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                             &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    });
-    return fn;
-}
-
-// The V array as the 3-D tensor the attention kernel copies sub-tiles of:
-// {row bytes, kv_bs rows, num_pages * nkv (page, head) pairs}, boxes of 32 rows.
-// q8 rows are 128 bytes (128-byte swizzle in shared memory), q4 rows 64 bytes
-// (64-byte swizzle).
-int set_vmap(AttnParams& p, bool q4 = false) {
-    const kq8_cache_t& c = p.cache;
-    const uint64_t pairs = (uint64_t)c.num_pages * (uint64_t)c.num_kv_heads;
-    if (pairs > 0x7FFFFFFFull) return KQ8_ERR_UNSUPPORTED;  // the copy's coordinate is int32
-    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
-    if (!enc) return KQ8_ERR_CUDA;
-    const cuuint64_t row = q4 ? HD / 2 : HD;
-    const cuuint64_t dims[3] = {row, (cuuint64_t)c.kv_bs, (cuuint64_t)pairs};
-    const cuuint64_t strides[2] = {row, (cuuint64_t)c.kv_bs * row};
-    const cuuint32_t box[3] = {(cuuint32_t)row, (cuuint32_t)TILE, 1u};
-    const cuuint32_t estr[3] = {1u, 1u, 1u};
-    const CUresult r = enc(&p.vmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, c.v, dims, strides, box,
-                           estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                           q4 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? KQ8_OK : KQ8_ERR_CUDA;
-}
-
 // The K array as the probe's 3-D tensor {1024 B: 32 positions x 32 B, 4 element
 // blocks, num_pages * nkv * kv_bs / 32 sub-tiles}, boxes of the first 8
 // positions of the 4 blocks (4 x 256 B), unswizzled.  Only for block = 4 *
@@ -269,15 +281,11 @@ void set_probe_kmap(SparseParams& sp) {
     const uint64_t subtiles =
         (uint64_t)c.num_pages * (uint64_t)c.num_kv_heads * (uint64_t)(c.kv_bs / TILE);
     if (subtiles == 0 || subtiles > 0x7FFFFFFFull) return;  // the copy's coordinate is int32
-    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
-    if (!enc) return;
-    const cuuint64_t dims[3] = {(cuuint64_t)TILE * 32, (cuuint64_t)NB, (cuuint64_t)subtiles};
-    const cuuint64_t strides[2] = {(cuuint64_t)TILE * 32, (cuuint64_t)TILE * HD};
-    const cuuint32_t box[3] = {8u * 32u, (cuuint32_t)NB, 1u};
-    const cuuint32_t estr[3] = {1u, 1u, 1u};
-    if (enc(&sp.kmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, c.k, dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS)
+    const uint64_t dims[3] = {(uint64_t)TILE * 32, (uint64_t)NB, subtiles};
+    const uint64_t strides[2] = {(uint64_t)TILE * 32, (uint64_t)TILE * HD};
+    const uint32_t box[3] = {8u * 32u, (uint32_t)NB, 1u};
+    if (encode_tensor_map(&sp.kmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, c.k, dims, strides, box,
+                          CU_TENSOR_MAP_SWIZZLE_NONE) == KQ8_OK)
         sp.probe_tma = 1;
 }
 
@@ -348,7 +356,7 @@ int run_sparse(float* out, const float* q, const kq8_cache_t* cache, const int32
     p.list_len = sp.list_len;
     p.list_cap = sp.list_cap;
     p.row_seq = row_seq;
-    rc = set_vmap(p);
+    rc = encode_vmap(&p.vmap, p.cache, false);
     if (rc) return rc;
     return launch_attn(p, G, true, rows, nkv, s);
 }
@@ -421,7 +429,7 @@ int kq8_decode_attn_q4(float* out, const float* q, const kq8_cache_t* cache,
     if (B == 0) return KQ8_OK;
     AttnParams p = attn_params(out, q, cache, page_table, max_pages, seq_lens, max_seq_len, B, nq,
                                scale, plan, workspace);
-    rc = set_vmap(p, true);
+    rc = encode_vmap(&p.vmap, p.cache, true);
     if (rc) return rc;
     return launch_attn_q4(p, nq / nkv, B, nkv, (cudaStream_t)stream);
 }
@@ -480,7 +488,7 @@ int kq8_decode_attn(float* out, const float* q, const kq8_cache_t* cache,
     if (B == 0) return KQ8_OK;
     AttnParams p = attn_params(out, q, cache, page_table, max_pages, seq_lens, max_seq_len, B, nq,
                                scale, plan, workspace);
-    rc = set_vmap(p);
+    rc = encode_vmap(&p.vmap, p.cache, false);
     if (rc) return rc;
     return launch_attn(p, nq / nkv, false, B, nkv, (cudaStream_t)stream);
 }
@@ -587,7 +595,7 @@ int kq8_decode_attn_update(float* state_acc, float* state_ms, const float* q,
     p.seq_begin = seq_begin;
     p.state_acc = state_acc;
     p.state_ms = reinterpret_cast<float2*>(state_ms);
-    rc = set_vmap(p);
+    rc = encode_vmap(&p.vmap, p.cache, false);
     if (rc) return rc;
     return launch_attn(p, nq / nkv, false, B, nkv, (cudaStream_t)stream);
 }
@@ -656,7 +664,7 @@ int kq8_debug_decode_withhold(float* out, const float* q, const kq8_cache_t* cac
     AttnParams p = attn_params(out, q, cache, page_table, max_pages, seq_lens, max_seq_len, B, nq,
                                scale, plan, workspace);
     p.withhold = withhold_tile;
-    rc = set_vmap(p);
+    rc = encode_vmap(&p.vmap, p.cache, false);
     if (rc) return rc;
     return launch_attn_withhold(p, nq / nkv, B, nkv, (cudaStream_t)stream);
 }
@@ -755,7 +763,7 @@ extern "C" int kq8_decode_attn_noalloc(float* out, const float* q, const kq8_cac
     // collects error bits that this entry point does not report.
     AttnParams p = attn_params(out, q, cache, page_table, max_pages, seq_lens, max_seq_len, B, nq,
                                scale, plan, ws);
-    rc = set_vmap(p);
+    rc = encode_vmap(&p.vmap, p.cache, false);
     if (rc) return rc;
     return launch_attn(p, nq / nkv, false, B, nkv, (cudaStream_t)stream);
 }

@@ -1,6 +1,7 @@
 // kq8_internal.h -- launchers shared between the libkq8 translation units.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "kq8.h"
@@ -11,9 +12,48 @@ struct AttnParams;
 struct SparseParams;
 struct PrefillParams;
 
+// Largest element stride a call takes (a token or head index times it stays
+// inside 64 bits).
+constexpr size_t MAX_STRIDE = (size_t)1 << 31;
+
+// kq8_write_kv / kq8_read_kv: rows of K and V outside the cache (element
+// strides, elements of a row adjacent) and the slot of each token.
+struct RowsParams {
+    kq8_cache_t cache;
+    void* k;
+    void* v;
+    int64_t k_st, k_sh, v_st, v_sh;
+    const int32_t* slot;
+    int32_t T;
+    uint32_t* status;
+};
+
+// kq8_tree_commit
+struct CommitParams {
+    kq8_cache_t cache;
+    const int32_t* page_table;
+    int32_t max_pages;
+    const int32_t* base_lens;
+    const int32_t* path;
+    const int32_t* path_len;
+    int32_t max_path;
+    uint32_t* status;
+};
+
 // Shared argument checks of a kq8_cache_t (head_dim 128, kv_bs a multiple of
 // 32 up to 256, 16-byte aligned arrays); returns a KQ8_ERR_* code or KQ8_OK.
 int check_cache_args(const kq8_cache_t* c);
+
+// The V array as the 3-D tensor map the attention kernels copy sub-tiles
+// through (see AttnParams::vmap); returns a KQ8_ERR_* code or KQ8_OK.
+int encode_vmap(CUtensorMap* map, const kq8_cache_t& c, bool q4);
+// cuTensorMapEncodeTiled for the library's other maps: rank, sizes, strides
+// (bytes, from dimension 1) and box of a tensor of `type`, with `swizzle`.
+int encode_tensor_map(CUtensorMap* map, CUtensorMapDataType type, uint32_t rank, void* base,
+                      const uint64_t* dims, const uint64_t* strides, const uint32_t* box,
+                      CUtensorMapSwizzle swizzle);
+// SMs of the current device (152 without one).
+int device_sms();
 
 int launch_append(const kq8_cache_t& c, const float* k, const float* v, const int32_t* slot,
                   int32_t T, uint32_t* status, cudaStream_t stream);

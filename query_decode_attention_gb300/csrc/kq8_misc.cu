@@ -2,47 +2,9 @@
 // test-only kernels that expose the hot path's integer building blocks.
 #include "kq8_common.cuh"
 #include "kq8_internal.h"
+#include "kq8_quant.cuh"
 
 namespace kq8 {
-
-// roundf(x / d) for the elements of a row whose step is d, |x / d| < 128, with
-// r = RN(1 / d).  r and the product q = RN(x * r) each round once (relative
-// 2^-24), so |q - x / d| <= 128 * 2^-23 and |fl(x / d) - x / d| <= 2^-18:
-// q is within 2^-15.5 of the IEEE quotient fl(x / d).  Unless q lies within
-// 2^-14 of a half-integer both therefore round to the same integer, and the
-// nearest integer to q (no tie possible) is roundf(fl(x / d)).  The rare
-// near-half case (about 1 in 8000 elements), and a non-finite q (d subnormal
-// or 0), take the IEEE quotient itself, so the result always equals the
-// method's roundf(x / d) bit for bit.
-// The nearest integer comes from adding 1.5 * 2^23 + off (exact for |q| < 2^22):
-// the sum's low byte is then (n + off) mod 256, the code byte itself.  On the
-// fast path |q| < 127.5 (and < 7.5 for q4), so no clamp is needed there.
-// Returns the lane's four code bytes (element i in byte i); r = RN(1 / d) (the
-// caller computes it once per row), lo / hi clamp the slow path, off is 0 (q8,
-// two's complement) or 8 (q4, offset binary).
-__device__ __forceinline__ uint32_t quantize4(const float4 x, float d, float r, float lo, float hi,
-                                              int off) {
-    const float magic = 12582912.0f + (float)off;  // 1.5 * 2^23 + off
-    const float q0 = __fmul_rn(x.x, r), q1 = __fmul_rn(x.y, r);
-    const float q2 = __fmul_rn(x.z, r), q3 = __fmul_rn(x.w, r);
-    const float t0 = __fadd_rn(q0, magic), t1 = __fadd_rn(q1, magic);
-    const float t2 = __fadd_rn(q2, magic), t3 = __fadd_rn(q3, magic);
-    const float far = 0.5f - 0x1p-14f;  // NaN / inf compare false
-    const bool ok = fabsf(q0 - (t0 - magic)) < far && fabsf(q1 - (t1 - magic)) < far &&
-                    fabsf(q2 - (t2 - magic)) < far && fabsf(q3 - (t3 - magic)) < far;
-    if (ok)
-        return __byte_perm(__byte_perm(__float_as_uint(t0), __float_as_uint(t1), 0x0040),
-                           __byte_perm(__float_as_uint(t2), __float_as_uint(t3), 0x0040), 0x5410);
-    auto slow = [&](float v) -> uint32_t {
-        const float n = fminf(fmaxf(roundf(__fdiv_rn(v, d)), lo), hi);
-        return (uint32_t)((int)n + off) & 0xffu;
-    };
-    return slow(x.x) | (slow(x.y) << 8) | (slow(x.z) << 16) | (slow(x.w) << 24);
-}
-
-__device__ __forceinline__ float absmax4(const float4 x) {
-    return fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w)));
-}
 
 // The q8 write path: one (token, KV head) row per group of LPR lanes, 32 / LPR
 // rows per warp (consecutive items: the heads of a token, whose fp32 rows are
@@ -201,27 +163,6 @@ __global__ void __launch_bounds__(APPEND_WARPS * 32)
         c.kscale[so] = mk;
         c.vscale[so] = mv;
     }
-}
-
-// The appends are programmatic launches: their CTAs may be scheduled while the
-// kernel before them (typically the previous layer's attention) finishes, and
-// wait for its completion before they read or write anything, so the stream
-// order of the call's effects is unchanged; only the launch latency overlaps.
-template <typename... KArgs, typename... Args>
-static int launch_pdl(void (*kern)(KArgs...), int64_t blocks, int threads, cudaStream_t stream,
-                      Args... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)blocks);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = 0;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kern, args...) != cudaSuccess) return KQ8_ERR_CUDA;
-    return cudaGetLastError() == cudaSuccess ? KQ8_OK : KQ8_ERR_CUDA;
 }
 
 int launch_append_q4(const kq8_cache_t& c, const float* k, const float* v, const int32_t* slot,

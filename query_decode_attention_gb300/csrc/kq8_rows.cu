@@ -1,0 +1,445 @@
+// kq8_rows.cu -- cache rows in and out: the write path for fp32 / fp16 / bf16
+// rows of any stride (article 9-3 §2, kv_quantize_per_head), the read back, and
+// the move of a draft tree's accepted path to its place behind the committed
+// tokens.
+//
+// Write and read.  A row is one (token, KV head) pair's 128 elements of K or V.
+// A block takes 32 consecutive tokens of one KV head: with consecutive slots
+// that is one K sub-tile and 32 V rows, 4 KB each, so every line of the pool
+// that the block touches it touches whole.  Within the block, group i of lanes
+// takes token krow(i): the groups of a warp then hold K rows at adjacent
+// positions of the sub-tile (32 bytes per position and element block).  A lane
+// holds 8 consecutive elements per chunk: one 16-byte access of a 16-bit row
+// (two of an fp32 row) and one 8-byte (q4: 4-byte) access of the pool, so a
+// packed q4 word (elements e .. e + 3 low, e + 4 .. e + 7 high) never crosses
+// lanes.  Both are bound by HBM: nothing is read or written twice.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <type_traits>
+
+#include "kq8_internal.h"
+#include "kq8_quant.cuh"
+
+namespace kq8 {
+
+namespace {
+
+constexpr int RW_LPR = 8;                 // lanes per row
+constexpr int RW_NC = HD / 8 / RW_LPR;    // 8-element chunks per lane
+constexpr int RW_THREADS = TILE * RW_LPR; // 32 tokens of one KV head
+
+struct Elem8 {
+    float4 a, b;
+};
+
+// 8 consecutive elements as fp32 (exact), and back with one rounding each.
+// VEC: 16-byte accesses (p is 16-byte aligned); else element by element.
+template <typename E>
+__device__ __forceinline__ float to_f32(E x);
+template <>
+__device__ __forceinline__ float to_f32(float x) { return x; }
+template <>
+__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
+template <>
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <typename E>
+__device__ __forceinline__ E from_f32(float x);
+template <>
+__device__ __forceinline__ float from_f32(float x) { return x; }
+template <>
+__device__ __forceinline__ __half from_f32(float x) { return __float2half_rn(x); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32(float x) { return __float2bfloat16_rn(x); }
+
+template <typename E, bool VEC>
+__device__ __forceinline__ Elem8 load8(const E* p) {
+    constexpr int W = (int)sizeof(E) * 8 / 16;  // 16-byte words
+    union {
+        uint4 w[W];
+        E e[8];
+    } u;
+    if constexpr (VEC) {
+#pragma unroll
+        for (int i = 0; i < W; i++) u.w[i] = __ldcs(reinterpret_cast<const uint4*>(p) + i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; i++) u.e[i] = p[i];
+    }
+    Elem8 r;
+    r.a = make_float4(to_f32(u.e[0]), to_f32(u.e[1]), to_f32(u.e[2]), to_f32(u.e[3]));
+    r.b = make_float4(to_f32(u.e[4]), to_f32(u.e[5]), to_f32(u.e[6]), to_f32(u.e[7]));
+    return r;
+}
+template <typename E, bool VEC>
+__device__ __forceinline__ void store8(E* p, const float (&x)[8]) {
+    constexpr int W = (int)sizeof(E) * 8 / 16;
+    union {
+        uint4 w[W];
+        E e[8];
+    } u;
+#pragma unroll
+    for (int i = 0; i < 8; i++) u.e[i] = from_f32<E>(x[i]);
+    if constexpr (VEC) {
+#pragma unroll
+        for (int i = 0; i < W; i++) __stcs(reinterpret_cast<uint4*>(p) + i, u.w[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; i++) p[i] = u.e[i];
+    }
+}
+
+// Where row r (0 .. kv_bs - 1) of (page, head) keeps elements e .. e + 7 (e a
+// multiple of 8): byte offsets into the K and V arrays.
+template <int BITS>
+__device__ __forceinline__ size_t k_off(int32_t page, int h, int nkv, int kv_bs, int r, int e) {
+    if constexpr (BITS == 8)
+        return kv_sub_off(page, h, nkv, kv_bs, r / TILE) + (size_t)(e >> 5) * 1024 +
+               (size_t)kpos(r % TILE) * 32 + (e & 31);
+    else
+        return kv4_sub_off(page, h, nkv, kv_bs, r / TILE) + (size_t)(e >> 5) * 512 +
+               (size_t)kpos(r % TILE) * 16 + ((e & 31) >> 1);
+}
+template <int BITS>
+__device__ __forceinline__ size_t v_off(int32_t page, int h, int nkv, int kv_bs, int r, int e) {
+    constexpr int ROW = BITS == 8 ? HD : HD / 2;
+    return (page_head(page, h, nkv) * (size_t)kv_bs + (size_t)r) * ROW + (BITS == 8 ? e : e / 2);
+}
+
+// The token, slot and checks shared by write and read: false where the group
+// has nothing to do.  Every lane of a group gets the same answer.
+struct RowAt {
+    int64_t t;
+    int32_t page;
+    int r, h, j;
+};
+__device__ __forceinline__ bool row_at(const RowsParams& P, RowAt& a) {
+    const int grp = threadIdx.x / RW_LPR;
+    a.j = threadIdx.x % RW_LPR;
+    a.h = blockIdx.y;
+    a.t = (int64_t)blockIdx.x * TILE + krow(grp);
+    if (a.t >= P.T) return false;
+    const int32_t sl = __ldg(P.slot + a.t);
+    if (sl < 0) return false;
+    if ((int64_t)sl >= (int64_t)P.cache.num_pages * P.cache.kv_bs) {
+        if (a.j == 0 && P.status) atomicOr(P.status, KQ8_STATUS_BAD_SLOT);
+        return false;
+    }
+    a.page = sl / P.cache.kv_bs;
+    a.r = sl - a.page * P.cache.kv_bs;
+    return true;
+}
+
+template <int BITS>
+__device__ __forceinline__ void put_codes(int8_t* dst, const Elem8& x, float d, float r, bool zero) {
+    constexpr float TOP = BITS == 8 ? 127.0f : 7.0f;
+    constexpr int OFF = BITS == 8 ? 0 : 8;
+    uint32_t lo = BITS == 8 ? 0u : 0x08080808u, hi = lo;
+    if (!zero) {
+        lo = quantize4(x.a, d, r, -TOP, TOP, OFF);
+        hi = quantize4(x.b, d, r, -TOP, TOP, OFF);
+    }
+    if constexpr (BITS == 8)
+        *reinterpret_cast<uint2*>(dst) = make_uint2(lo, hi);
+    else
+        *reinterpret_cast<uint32_t*>(dst) = lo | (hi << 4);
+}
+
+// The write rule on the row widened to fp32, so the codes and maxima equal
+// kq8_append_kv's for the same values bit for bit.
+template <typename E, int BITS, bool VEC>
+__global__ void __launch_bounds__(RW_THREADS) kq8_write_kernel(const RowsParams P) {
+    griddep_wait();
+    griddep_launch_dependents();
+    RowAt at;
+    const bool on = row_at(P, at);
+    Elem8 x[2][RW_NC];
+    float m[2] = {0.0f, 0.0f};
+    if (on) {
+        const E* src[2] = {
+            static_cast<const E*>(P.k) + at.t * P.k_st + at.h * P.k_sh,
+            static_cast<const E*>(P.v) + at.t * P.v_st + at.h * P.v_sh};
+#pragma unroll
+        for (int s = 0; s < 2; s++)
+#pragma unroll
+            for (int i = 0; i < RW_NC; i++)
+                x[s][i] = load8<E, VEC>(src[s] + 8 * (RW_LPR * i + at.j));
+#pragma unroll
+        for (int s = 0; s < 2; s++)
+#pragma unroll
+            for (int i = 0; i < RW_NC; i++)
+                m[s] = fmaxf(m[s], fmaxf(absmax4(x[s][i].a), absmax4(x[s][i].b)));
+    }
+#pragma unroll
+    for (int o = 1; o < RW_LPR; o <<= 1)
+#pragma unroll
+        for (int s = 0; s < 2; s++) m[s] = fmaxf(m[s], __shfl_xor_sync(0xffffffffu, m[s], o));
+    if (!on) return;
+    const int nkv = P.cache.num_kv_heads, kv_bs = P.cache.kv_bs;
+#pragma unroll
+    for (int s = 0; s < 2; s++) {
+        const float d = __fmul_rn(m[s], BITS == 8 ? inv127() : inv7()), r = __frcp_rn(d);
+#pragma unroll
+        for (int i = 0; i < RW_NC; i++) {
+            const int e = 8 * (RW_LPR * i + at.j);
+            int8_t* dst = s == 0 ? P.cache.k + k_off<BITS>(at.page, at.h, nkv, kv_bs, at.r, e)
+                                 : P.cache.v + v_off<BITS>(at.page, at.h, nkv, kv_bs, at.r, e);
+            put_codes<BITS>(dst, x[s][i], d, r, m[s] == 0.0f);
+        }
+    }
+    if (at.j == 0) {
+        const size_t so = page_head(at.page, at.h, nkv) * (size_t)kv_bs + at.r;
+        P.cache.kscale[so] = m[0];
+        P.cache.vscale[so] = m[1];
+    }
+}
+
+// 8 codes -> 8 fp32 values (exact).
+template <int BITS>
+__device__ __forceinline__ void get_codes(const int8_t* src, float (&c)[8]) {
+    if constexpr (BITS == 8) {
+        const uint2 w = __ldcs(reinterpret_cast<const uint2*>(src));
+        i8x4_to_f32(w.x, c[0], c[1], c[2], c[3]);
+        i8x4_to_f32(w.y, c[4], c[5], c[6], c[7]);
+    } else {
+        const uint32_t w = __ldcs(reinterpret_cast<const uint32_t*>(src));
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            c[i] = (float)((int)((w >> (8 * (i & 3) + 4 * (i >> 2))) & 15u) - 8);
+    }
+}
+
+// The values the rows stand for: code * (stored max * (1/127)) (q4: 1/7), one
+// fp32 product as the attention kernels' readers form it, then one rounding to
+// the output type.
+template <typename E, int BITS, bool VEC>
+__global__ void __launch_bounds__(RW_THREADS) kq8_read_kernel(const RowsParams P) {
+    griddep_wait();
+    griddep_launch_dependents();
+    RowAt at;
+    if (!row_at(P, at)) return;
+    const int nkv = P.cache.num_kv_heads, kv_bs = P.cache.kv_bs;
+    const size_t so = page_head(at.page, at.h, nkv) * (size_t)kv_bs + at.r;
+    float c[2][RW_NC][8];
+#pragma unroll
+    for (int i = 0; i < RW_NC; i++) {
+        const int e = 8 * (RW_LPR * i + at.j);
+        get_codes<BITS>(P.cache.k + k_off<BITS>(at.page, at.h, nkv, kv_bs, at.r, e), c[0][i]);
+        get_codes<BITS>(P.cache.v + v_off<BITS>(at.page, at.h, nkv, kv_bs, at.r, e), c[1][i]);
+    }
+    const float inv = BITS == 8 ? inv127() : inv7();
+    const float d[2] = {__fmul_rn(P.cache.kscale[so], inv), __fmul_rn(P.cache.vscale[so], inv)};
+    E* dst[2] = {static_cast<E*>(P.k) + at.t * P.k_st + at.h * P.k_sh,
+                 static_cast<E*>(P.v) + at.t * P.v_st + at.h * P.v_sh};
+#pragma unroll
+    for (int s = 0; s < 2; s++)
+#pragma unroll
+        for (int i = 0; i < RW_NC; i++) {
+            float y[8];
+#pragma unroll
+            for (int k = 0; k < 8; k++) y[k] = __fmul_rn(c[s][i][k], d[s]);
+            store8<E, VEC>(dst[s] + 8 * (RW_LPR * i + at.j), y);
+        }
+}
+
+// ---------------------------------------------------------------------------
+// The accepted path of a draft tree: of sequence b's drafts, which sit at
+// positions base .. in the order they were written, draft path[i] moves to
+// position base + i, for i < len.  The path ascends strictly (a tree's nodes
+// follow their parents), so path[i] >= i: a block that takes the rows in order,
+// a batch at a time, loads a batch before it stores it, and never stores over a
+// row that a later batch loads (its sources lie at or behind the batch's own
+// first position, and every earlier store before it).  Codes and maxima move
+// bit for bit.  One block per (sequence, KV head); 16 lanes move a row: lanes
+// 0-7 K, 8-15 V, a 16-byte (q4: 8-byte) piece each.
+// A path with a bad entry, position or page moves nothing and sets a status
+// bit; every block of the sequence checks the whole path, so all agree.
+// ---------------------------------------------------------------------------
+constexpr int CM_THREADS = 256;
+constexpr int CM_ROWS = CM_THREADS / 16;
+
+template <int BITS>
+__global__ void __launch_bounds__(CM_THREADS) kq8_commit_kernel(const CommitParams P) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
+    const int nkv = P.cache.num_kv_heads, kv_bs = P.cache.kv_bs;
+    const int32_t base = P.base_lens[b], len = P.path_len[b];
+    const int64_t room = (int64_t)P.max_pages * kv_bs;
+    const int32_t* path = P.path + (size_t)b * P.max_path;
+    const int32_t* table = P.page_table + (size_t)b * P.max_pages;
+    uint32_t bad = 0;
+    if (base < 0 || len < 0 || len > P.max_path) {
+        bad = KQ8_STATUS_BAD_SEQLEN;
+    } else {
+        for (int i = tid; i < len; i += CM_THREADS) {
+            const int32_t j = path[i];
+            if (j < 0 || (i > 0 && path[i - 1] >= j) || (int64_t)base + j >= room) {
+                bad |= KQ8_STATUS_BAD_SEQLEN;
+                continue;
+            }
+            const int32_t p0 = table[(base + j) / kv_bs];
+            if (p0 < 0 || p0 >= P.cache.num_pages) bad |= KQ8_STATUS_BAD_PAGE;
+            if ((int64_t)base + i < room) {  // j >= i on a good path
+                const int32_t p1 = table[(base + i) / kv_bs];
+                if (p1 < 0 || p1 >= P.cache.num_pages) bad |= KQ8_STATUS_BAD_PAGE;
+            }
+        }
+    }
+    if (bad && P.status) atomicOr(P.status, bad);
+    if (__syncthreads_or(bad != 0)) return;
+    using Piece = typename std::conditional<BITS == 8, uint4, uint2>::type;
+    const int l = tid & 15, e = (l & 7) * 16;  // this lane's 16 elements
+    for (int i0 = 0; i0 < len; i0 += CM_ROWS) {
+        const int i = i0 + (tid >> 4);
+        const int32_t j = i < len ? path[i] : i;
+        const bool moves = j != i;
+        Piece piece;
+        float scale = 0.0f;
+        auto place = [&](int32_t pos, int8_t*& codes, float*& s) {
+            const int32_t page = table[pos / kv_bs];
+            const int r = pos % kv_bs;
+            codes = l < 8 ? P.cache.k + k_off<BITS>(page, h, nkv, kv_bs, r, e)
+                          : P.cache.v + v_off<BITS>(page, h, nkv, kv_bs, r, e);
+            s = (l < 8 ? P.cache.kscale : P.cache.vscale) +
+                page_head(page, h, nkv) * (size_t)kv_bs + r;
+        };
+        int8_t* codes;
+        float* s;
+        if (moves) {
+            place(base + j, codes, s);
+            piece = *reinterpret_cast<const Piece*>(codes);
+            if ((l & 7) == 0) scale = *s;
+        }
+        __syncthreads();  // the batch is loaded before any of it is stored
+        if (moves) {
+            place(base + i, codes, s);
+            *reinterpret_cast<Piece*>(codes) = piece;
+            if ((l & 7) == 0) *s = scale;
+        }
+        __syncthreads();  // stored before the next batch loads
+    }
+}
+
+template <bool WRITE, typename E, int BITS>
+int launch_rows_t(const RowsParams& p, bool vec, cudaStream_t s) {
+    const dim3 grid((unsigned)(((int64_t)p.T + TILE - 1) / TILE), (unsigned)p.cache.num_kv_heads);
+    if constexpr (WRITE)
+        return vec ? launch_pdl(kq8_write_kernel<E, BITS, true>, grid, RW_THREADS, s, p)
+                   : launch_pdl(kq8_write_kernel<E, BITS, false>, grid, RW_THREADS, s, p);
+    else
+        return vec ? launch_pdl(kq8_read_kernel<E, BITS, true>, grid, RW_THREADS, s, p)
+                   : launch_pdl(kq8_read_kernel<E, BITS, false>, grid, RW_THREADS, s, p);
+}
+
+template <bool WRITE, int BITS>
+int launch_rows(const RowsParams& p, int dtype, bool vec, cudaStream_t s) {
+    switch (dtype) {
+        case KQ8_F32: return launch_rows_t<WRITE, float, BITS>(p, vec, s);
+        case KQ8_F16: return launch_rows_t<WRITE, __half, BITS>(p, vec, s);
+        default: return launch_rows_t<WRITE, __nv_bfloat16, BITS>(p, vec, s);
+    }
+}
+
+// Whether n1 x n2 rows of HD elements at strides s1 and s2 do not overlap (the
+// larger stride steps over all rows of the smaller one).
+bool rows_apart(int64_t s1, int64_t n1, int64_t s2, int64_t n2) {
+    if (n1 <= 1) return n2 <= 1 || s2 >= HD;
+    if (n2 <= 1) return s1 >= HD;
+    if (s1 > s2) return rows_apart(s2, n2, s1, n1);
+    return s1 >= HD && s2 >= (n1 - 1) * s1 + HD;
+}
+
+// Checks, the choice of 16-byte accesses (bases and strides multiples of 16
+// bytes), launch.
+template <bool WRITE>
+int rows_impl(const kq8_cache_t* cache, int32_t bits, void* k, void* v, int32_t dtype,
+              size_t k_st, size_t k_sh, size_t v_st, size_t v_sh, const int32_t* slot, int32_t T, uint32_t* status, kq8_stream_t stream) {
+    int rc = check_cache_args(cache);
+    if (rc) return rc;
+    if (bits != 8 && bits != 4) return KQ8_ERR_UNSUPPORTED;
+    if (dtype != KQ8_F32 && dtype != KQ8_F16 && dtype != KQ8_BF16) return KQ8_ERR_UNSUPPORTED;
+    if (cache->num_kv_heads > 65535) return KQ8_ERR_UNSUPPORTED;
+    if (T < 0) return KQ8_ERR_INVALID_ARG;
+    if (T == 0) return KQ8_OK;
+    const size_t es = dtype == KQ8_F32 ? 4 : 2;
+    if (!k || !v || !slot || (uintptr_t)k % es || (uintptr_t)v % es || (uintptr_t)slot % 4)
+        return KQ8_ERR_INVALID_ARG;
+    if (status && (uintptr_t)status % 4) return KQ8_ERR_INVALID_ARG;
+    const size_t st[4] = {k_st, k_sh, v_st, v_sh};
+    bool vec = (uintptr_t)k % 16 == 0 && (uintptr_t)v % 16 == 0;
+    for (size_t x : st) {
+        if (x > MAX_STRIDE) return KQ8_ERR_INVALID_ARG;
+        vec = vec && (x * es) % 16 == 0;
+    }
+    // the rows a read stores must not overlap
+    const int64_t heads = cache->num_kv_heads;
+    if (!WRITE && (!rows_apart((int64_t)k_st, T, (int64_t)k_sh, heads) ||
+                   !rows_apart((int64_t)v_st, T, (int64_t)v_sh, heads)))
+        return KQ8_ERR_INVALID_ARG;
+    RowsParams p;
+    p.cache = *cache;
+    p.k = k;
+    p.v = v;
+    p.k_st = (int64_t)k_st;
+    p.k_sh = (int64_t)k_sh;
+    p.v_st = (int64_t)v_st;
+    p.v_sh = (int64_t)v_sh;
+    p.slot = slot;
+    p.T = T;
+    p.status = status;
+    return bits == 8 ? launch_rows<WRITE, 8>(p, dtype, vec, (cudaStream_t)stream)
+                     : launch_rows<WRITE, 4>(p, dtype, vec, (cudaStream_t)stream);
+}
+
+}  // namespace
+}  // namespace kq8
+
+using namespace kq8;
+
+extern "C" {
+
+int kq8_write_kv(const kq8_cache_t* cache, int32_t bits, const void* k, const void* v,
+                 int32_t dtype, size_t k_token_stride, size_t k_head_stride,
+                 size_t v_token_stride, size_t v_head_stride, const int32_t* slot, int32_t T,
+                 uint32_t* status, kq8_stream_t stream) {
+    return rows_impl<true>(cache, bits, const_cast<void*>(k), const_cast<void*>(v), dtype,
+                           k_token_stride, k_head_stride, v_token_stride, v_head_stride, slot, T,
+                           status, stream);
+}
+
+int kq8_read_kv(const kq8_cache_t* cache, int32_t bits, void* k, void* v, int32_t dtype,
+                size_t k_token_stride, size_t k_head_stride, size_t v_token_stride,
+                size_t v_head_stride, const int32_t* slot, int32_t T, uint32_t* status,
+                kq8_stream_t stream) {
+    return rows_impl<false>(cache, bits, k, v, dtype, k_token_stride, k_head_stride,
+                            v_token_stride, v_head_stride, slot, T, status, stream);
+}
+
+int kq8_tree_commit(const kq8_cache_t* cache, int32_t bits, const int32_t* page_table,
+                    int32_t max_pages, const int32_t* base_lens, const int32_t* path,
+                    const int32_t* path_len, int32_t max_path, int32_t B, uint32_t* status,
+                    kq8_stream_t stream) {
+    int rc = check_cache_args(cache);
+    if (rc) return rc;
+    if (bits != 8 && bits != 4) return KQ8_ERR_UNSUPPORTED;
+    if (B < 0 || max_path < 0 || max_pages < 0) return KQ8_ERR_INVALID_ARG;
+    if (B > 65535 || (int64_t)max_pages * cache->kv_bs >= (1 << 29)) return KQ8_ERR_UNSUPPORTED;
+    if (status && (uintptr_t)status % 4) return KQ8_ERR_INVALID_ARG;
+    if (B == 0 || max_path == 0) return KQ8_OK;
+    if (!page_table || !base_lens || !path || !path_len) return KQ8_ERR_INVALID_ARG;
+    CommitParams p;
+    p.cache = *cache;
+    p.page_table = page_table;
+    p.max_pages = max_pages;
+    p.base_lens = base_lens;
+    p.path = path;
+    p.path_len = path_len;
+    p.max_path = max_path;
+    p.status = status;
+    const dim3 grid((unsigned)cache->num_kv_heads, (unsigned)B);
+    return bits == 8 ? launch_pdl(kq8_commit_kernel<8>, grid, CM_THREADS, (cudaStream_t)stream, p)
+                     : launch_pdl(kq8_commit_kernel<4>, grid, CM_THREADS, (cudaStream_t)stream, p);
+}
+
+}  // extern "C"

@@ -1,0 +1,714 @@
+// kq8_tree.cu -- attention for trees of drafted tokens over the paged q8 cache.
+//
+// Speculative decoding writes the nb drafts of a sequence behind its committed
+// tokens and asks, in one call, what every draft would attend: the committed
+// tokens (base = n - nb of them) and the drafts on its own branch, given as a
+// bit mask.  Each (node, query head) row is computed like one decode query
+// (article 9-2 §2): Q quantised once in 32-element max-abs blocks, score =
+// ((sum_b dot_b * qsc_b) * ks) * scale with exact integer block dots, a one-pass
+// softmax, one divide at the end.
+//
+// Work decomposition: CTA = (KV chunk, tile of 16 rows, KV head, sequence), 4
+// warps.  The rows of a KV head are its G query heads of every node.  As in the
+// decode kernel each warp owns a two-stage ring of 32-token sub-tiles filled by
+// bulk and tensor copies, and takes every fourth sub-tile of its chunk; chunks
+// are merged by the last CTA to finish (a ticket).  Per sub-tile, on the warp's
+// matrix instructions (m16n8k16, fp16 in, fp32 out):
+//   scores: 4 groups of 8 tokens x 4 element blocks x 2 k-steps.  The codes of
+//     Q and K are exact in fp16 and a block dot is below 2^19, so each fp32
+//     accumulator is the exact integer block dot; the blocks' Q scales follow
+//     as fp32 multiply-adds.
+//   values: the weights p * vstep as fp16 (hi + lo, 22 significant bits, for
+//     fp32 and fp16 outputs; hi alone for bf16 outputs, whose own rounding is
+//     16 times coarser) times the V codes, exact in fp16.
+// Token order.  Lane (g, c) of the score accumulators holds rows g, g + 8 and
+// columns 2c, 2c + 1 of each 8-token group.  Column n of group i is token
+//   tok(i, n) = 4 n + (i + n / 2) % 4,
+// which is K position 8 ((i + n / 2) % 4) + n: the eight 32-byte pieces that a
+// group reads lie in different banks, and lane c's tokens of group i are the
+// two that the same lane needs for k-columns of the value product, where the
+// eight V rows of a transposed 8 x 8 load are tok(i, 0..7): all different
+// modulo 8, so the 128-byte swizzle keeps that load free of conflicts too.
+// The weights therefore go from accumulators to operands within the lane.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstring>
+#include <type_traits>
+
+#include "kq8_internal.h"
+#include "kq8_common.cuh"
+
+namespace kq8 {
+namespace {
+
+constexpr int TR_WARPS = 4;
+constexpr int TR_THREADS = TR_WARPS * 32;
+constexpr int TR_STAGES = 2;
+constexpr int TR_ROWS = 16;
+constexpr int TR_MAX_CHUNK = 128;       // sub-tiles per chunk, see tree_plan
+constexpr float TR_LOG2E = 1.4426950408889634f;
+// Lazy rescale: between rescales a weight stays below 2^TR_SLACK.
+constexpr float TR_SLACK = 8.0f;
+
+constexpr size_t TR_STATUS_BYTES = 256;
+constexpr size_t TR_COUNTERS = 16384;
+constexpr size_t TR_HEADER = TR_STATUS_BYTES + TR_COUNTERS * sizeof(uint32_t);
+
+struct TreeParams {
+    CUtensorMap vmap;
+    void* out;
+    const void* q;
+    int64_t q_st, q_sh;  // element strides of q's tokens and heads
+    int32_t dtype;
+    int32_t total_q;
+    kq8_cache_t cache;
+    const int32_t* page_table;
+    int32_t max_pages;
+    const int32_t* seq_lens;
+    const int32_t* q_off;
+    const uint32_t* mask;  // [total_q][mask_words]; null: node i sees nodes 0 .. i
+    int32_t mask_words;
+    int32_t max_seq_len, max_q_len;
+    int32_t b0;            // first sequence of this launch
+    int32_t nq, G;
+    float scale;
+    int32_t chunk_tiles, num_chunks, row_tiles;
+    float* part_acc;       // [pairs][16][num_chunks][HD]
+    float2* part_ms;       // [pairs][16][num_chunks]
+    uint32_t* status;
+    uint32_t* counters;    // [pairs]
+};
+
+struct TreeSmem {
+    alignas(1024) uint8_t v[TR_WARPS][TR_STAGES][SUB_V_BYTES];
+    alignas(128) uint8_t k[TR_WARPS][TR_STAGES][SUB_K_BYTES];
+    alignas(16) float sc[TR_WARPS][TR_STAGES][2][TILE];  // kscale, vscale as stored
+    alignas(16) float mul[TR_WARPS][2][TILE];            // score multiplier, weight multiplier
+    alignas(16) int8_t qi[TR_ROWS][HD];
+    alignas(16) float qsc[TR_ROWS][NB];
+    alignas(16) float2 ms[TR_WARPS][TR_ROWS];
+    alignas(8) uint64_t bar[TR_WARPS][TR_STAGES];
+    int last;
+};
+
+__device__ __forceinline__ float tr_ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 4 elements of a q row as fp32 (exact).
+__device__ __forceinline__ float4 load_q4(const void* q, int dtype, int64_t at) {
+    if (dtype == KQ8_F32) return *reinterpret_cast<const float4*>(static_cast<const float*>(q) + at);
+    const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(q) + at);
+    if (dtype == KQ8_F16) {
+        const float2 a = h2_to_f2(w.x), b = h2_to_f2(w.y);
+        return make_float4(a.x, a.y, b.x, b.y);
+    }
+    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u),
+                       __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u));
+}
+// One rounding to the output type.
+__device__ __forceinline__ void store_out4(void* out, int dtype, size_t at, const float4 x) {
+    if (dtype == KQ8_F32) {
+        *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = x;
+    } else if (dtype == KQ8_F16) {
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) =
+            make_uint2(f2_to_h2(x.x, x.y), f2_to_h2(x.z, x.w));
+    } else {
+        __nv_bfloat162 a = __floats2bfloat162_rn(x.x, x.y), b = __floats2bfloat162_rn(x.z, x.w);
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) =
+            make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
+    }
+}
+
+// What node i of a sequence with nb nodes sees among nodes jt .. jt + 31, as
+// bits; a negative node index is a committed token (always seen), one past the
+// last node never is.
+__device__ __forceinline__ uint32_t node_window(const TreeParams& P, int64_t row0, int i, int nb,
+                                                int jt) {
+    auto word = [&](int w) -> uint32_t {
+        if (w < 0) return 0xFFFFFFFFu;
+        const int j0 = 32 * w;
+        if (j0 >= nb) return 0u;
+        uint32_t x;
+        if (P.mask)
+            x = P.mask[(row0 + i) * P.mask_words + w];
+        else
+            x = i >= j0 + 31 ? 0xFFFFFFFFu : (i < j0 ? 0u : (2u << (i - j0)) - 1u);
+        return nb >= j0 + 32 ? x : x & ((1u << (nb - j0)) - 1u);
+    };
+    const int w = jt >> 5, s = jt & 31;  // floor division
+    return __funnelshift_r(word(w), s ? word(w + 1) : 0u, s);
+}
+
+template <bool HILO>
+__global__ void __launch_bounds__(TR_THREADS, 3)
+    kq8_tree_kernel(const __grid_constant__ TreeParams P) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    TreeSmem& S = *reinterpret_cast<TreeSmem*>(
+        smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int gq = lane >> 2, c4 = lane & 3;
+    const int rt = blockIdx.x % P.row_tiles, chunk = blockIdx.x / P.row_tiles;
+    const int h = blockIdx.y, b = P.b0 + blockIdx.z;
+    const int nkv = P.cache.num_kv_heads, kv_bs = P.cache.kv_bs, subs = kv_bs / TILE;
+    const int G = P.G;
+
+    if (threadIdx.x == 0)
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&P.vmap))
+                     : "memory");
+    if (lane == 0)
+        for (int s = 0; s < TR_STAGES; s++) mbar_init(&S.bar[warp][s], 1);
+    fence_barrier_init();
+    // nothing is read or written before the kernel before this one has
+    // completed; the next one waits for this grid in the same way
+    griddep_wait();
+    griddep_launch_dependents();
+
+    const int n = P.seq_lens[b];
+    const int q0 = P.q_off[b];
+    const int nb = P.q_off[b + 1] - q0;
+    if (n < 0 || n > P.max_seq_len || nb < 0 || nb > n || nb > P.max_q_len || q0 < 0 ||
+        (int64_t)q0 + nb > P.total_q) {
+        if (threadIdx.x == 0 && blockIdx.x == 0 && h == 0) atomicOr(P.status, KQ8_STATUS_BAD_SEQLEN);
+        return;
+    }
+    const int base = n - nb;
+    const int rows = min(TR_ROWS, nb * G - rt * TR_ROWS);  // of this row tile
+    if (rows <= 0) return;
+    const int tiles = (n + TILE - 1) / TILE;  // n >= nb >= 1 here
+    const int nch = (tiles + P.chunk_tiles - 1) / P.chunk_tiles;
+    if (chunk >= nch) return;
+    const int ce = min(P.chunk_tiles, tiles - chunk * P.chunk_tiles);
+    const int mine = ce > warp ? (ce - warp + TR_WARPS - 1) / TR_WARPS : 0;
+    const int first = chunk * P.chunk_tiles + warp;  // this warp's tiles: first + 4 i
+
+    // page ids of this warp's tiles, one per lane for a window of 32, the next
+    // window fetched a window ahead
+    auto load_window = [&](int w) -> int32_t {
+        const int i = 32 * w + lane;
+        if (i >= mine) return -1;
+        const int32_t pg = P.page_table[(size_t)b * P.max_pages + (first + TR_WARPS * i) / subs];
+        if (pg >= 0 && pg < P.cache.num_pages) return pg;
+        atomicOr(P.status, KQ8_STATUS_BAD_PAGE);
+        return -1;
+    };
+    int32_t page_cur = load_window(0), page_nxt = load_window(1);
+    int window = 0;
+    auto page_of = [&](int i) -> int32_t {
+        return __shfl_sync(0xffffffffu, (i >> 5) == window ? page_cur : page_nxt, i & 31);
+    };
+    __syncthreads();  // barriers initialised
+    const uint64_t pol = l2_evict_first_policy();
+    auto issue = [&](int i) {
+        const int tile = first + TR_WARPS * i;
+        const int32_t pg = page_of(i);
+        if (lane != 0) return;
+        const int s = i % TR_STAGES;
+        uint64_t* bar = &S.bar[warp][s];
+        if (pg < 0) {
+            mbar_arrive_expect_tx(bar, 0);  // completes the phase with no data
+            return;
+        }
+        const int sub = tile % subs;
+        const size_t so = scale_sub_off(pg, h, nkv, kv_bs, sub);
+        mbar_arrive_expect_tx(bar, STAGE_BYTES);
+        bulk_g2s(S.k[warp][s], P.cache.k + kv_sub_off(pg, h, nkv, kv_bs, sub), SUB_K_BYTES, bar,
+                 pol);
+        tma_load_3d(S.v[warp][s], &P.vmap, 0, sub * TILE, (int)page_head(pg, h, nkv), bar, pol);
+        bulk_g2s(S.sc[warp][s][0], P.cache.kscale + so, SUB_S_BYTES, bar, pol);
+        bulk_g2s(S.sc[warp][s][1], P.cache.vscale + so, SUB_S_BYTES, bar, pol);
+    };
+    for (int i = 0; i < TR_STAGES && i < mine; i++) issue(i);
+
+    // ---- Q's codes while the first copies are in flight (article 9-2 §2 seg. 1)
+    for (int r = warp; r < TR_ROWS; r += TR_WARPS) {
+        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (r < rows) {
+            const int rr = rt * TR_ROWS + r, node = rr / G, hq = h * G + rr % G;
+            x = load_q4(P.q, P.dtype, (int64_t)(q0 + node) * P.q_st + hq * P.q_sh + 4 * lane);
+        }
+        float qs;
+        const uint32_t codes = quantize_q_lane(x, qs);
+        reinterpret_cast<uint32_t*>(S.qi[r])[lane] = codes;
+        if ((lane & 7) == 0) S.qsc[r][lane >> 3] = qs;
+    }
+    __syncthreads();
+    // A operand of the scores: k-step s of block bb takes elements 8c + 4s ..
+    // + 3 of the block (K's pieces are read in the same order)
+    uint32_t qa[NB][2][4];
+    float qsc[2][NB];
+#pragma unroll
+    for (int half = 0; half < 2; half++)
+#pragma unroll
+        for (int bb = 0; bb < NB; bb++) {
+            qsc[half][bb] = S.qsc[gq + 8 * half][bb];
+            const uint2 w = *reinterpret_cast<const uint2*>(&S.qi[gq + 8 * half][bb * 32 + 8 * c4]);
+            const uint32_t u[2] = {w.x ^ 0x80808080u, w.y ^ 0x80808080u};
+#pragma unroll
+            for (int s = 0; s < 2; s++) {
+                qa[bb][s][half] = hsub2(__byte_perm(u[s], 0x64646464u, 0x4140), 0x64806480u);
+                qa[bb][s][half + 2] = hsub2(__byte_perm(u[s], 0x64646464u, 0x4342), 0x64806480u);
+            }
+        }
+
+    // rows gq and gq + 8: running max (base 2), partial sum over this lane's
+    // tokens; O: D[cg][0] elements 16cg + 2j, D[cg][1] 16cg + 2j + 1 (column j)
+    float M[2] = {M_INIT, M_INIT}, sum[2] = {0.0f, 0.0f};
+    float D[HD / 16][2][4];
+#pragma unroll
+    for (int cg = 0; cg < HD / 16; cg++)
+#pragma unroll
+        for (int j = 0; j < 4; j++) D[cg][0][j] = D[cg][1][j] = 0.0f;
+    // the weights of row half go to the matrix instructions scaled by 2^-ev[half];
+    // per row, so that what a row does not see cannot cost it precision
+    int ev[2] = {-126, -126};
+    const float kmul = inv127() * P.scale * TR_LOG2E;
+
+    auto step = [&](int st, int tile, auto masked_c) {
+        constexpr bool MASKED = decltype(masked_c)::value;
+        const uint8_t* kst = S.k[warp][st];
+        uint32_t win[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};  // visible tokens of the two rows
+        if (MASKED) {
+#pragma unroll
+            for (int half = 0; half < 2; half++) {
+                const int r = gq + 8 * half;
+                win[half] = r < rows ? node_window(P, q0, (rt * TR_ROWS + r) / G, nb,
+                                                   tile * TILE - base)
+                                     : 0u;
+            }
+        }
+        // lane = token: its score multiplier and V step.  A token past the end gets
+        // 0 for both: what its row of the page holds must not matter.
+        const bool live = !MASKED || tile * TILE + lane < n;
+        const float vstep = live ? __fmul_rn(S.sc[warp][st][1][lane], inv127()) : 0.0f;
+        S.mul[warp][0][lane] = live ? __fmul_rn(S.sc[warp][st][0][lane], kmul) : 0.0f;
+        S.mul[warp][1][lane] = vstep;
+        __syncwarp();
+        float2 km[4], vm[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const int t = 8 * c4 + ((i + c4) & 3);
+            km[i] = make_float2(S.mul[warp][0][t], S.mul[warp][0][t + 4]);
+            vm[i] = make_float2(S.mul[warp][1][t], S.mul[warp][1][t + 4]);
+        }
+        // ev keeps the largest V step that the row sees times 2^-ev below 2^7, so with
+        // p <= 2^8 a weight stays below 2^15, inside the fp16 range; a tile that needs
+        // a larger ev first scales the row of O by the exact power of two 2^(old - new).
+        // A step that is not finite does not count: its row is lost where it is seen.
+        {
+            auto bits = [](float x) -> uint32_t {
+                const uint32_t u = __float_as_uint(x) & 0x7FFFFFFFu;
+                return u < 0x7F800000u ? u : 0u;
+            };
+            uint32_t vb[2];
+            if (!MASKED) {
+                vb[0] = vb[1] = __reduce_max_sync(0xffffffffu, bits(vstep));
+            } else {
+#pragma unroll
+                for (int half = 0; half < 2; half++) {
+                    vb[half] = 0u;
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        const int t = 8 * c4 + ((i + c4) & 3);
+                        if ((win[half] >> t) & 1u) vb[half] = max(vb[half], bits(vm[i].x));
+                        if ((win[half] >> (t + 4)) & 1u) vb[half] = max(vb[half], bits(vm[i].y));
+                    }
+                    vb[half] = max(vb[half], __shfl_xor_sync(0xffffffffu, vb[half], 1));
+                    vb[half] = max(vb[half], __shfl_xor_sync(0xffffffffu, vb[half], 2));
+                }
+            }
+            const int en[2] = {max(ev[0], (int)(vb[0] >> 23) - 133), max(ev[1], (int)(vb[1] >> 23) - 133)};
+            if (__any_sync(0xffffffffu, en[0] != ev[0] || en[1] != ev[1])) {  // rare
+#pragma unroll
+                for (int half = 0; half < 2; half++) {
+                    const float f = (ev[half] - en[half] >= -126) ? pow2i(ev[half] - en[half]) : 0.0f;
+#pragma unroll
+                    for (int cg = 0; cg < HD / 16; cg++)
+#pragma unroll
+                        for (int j = 0; j < 2; j++) {
+                            D[cg][j][2 * half] *= f;
+                            D[cg][j][2 * half + 1] *= f;
+                        }
+                    ev[half] = en[half];
+                }
+            }
+        }
+        const float vsc[2] = {pow2i(-ev[0]), pow2i(-ev[1])};
+        // ---- scores: s[i][half] = (token 8c + r_i, token 8c + 4 + r_i), r_i = (i + c) % 4
+        float2 s[4][2];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const uint8_t* kp = kst + (8 * ((i + (gq >> 1)) & 3) + gq) * 32 + 8 * c4;
+#pragma unroll
+            for (int bb = 0; bb < NB; bb++) {
+                const uint2 w = *reinterpret_cast<const uint2*>(kp + 1024 * bb);
+                const uint32_t u0 = w.x ^ 0x80808080u, u1 = w.y ^ 0x80808080u;
+                float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                mma_f16_16816(d, qa[bb][0],
+                              hsub2(__byte_perm(u0, 0x64646464u, 0x4140), 0x64806480u),
+                              hsub2(__byte_perm(u0, 0x64646464u, 0x4342), 0x64806480u));
+                mma_f16_16816(d, qa[bb][1],
+                              hsub2(__byte_perm(u1, 0x64646464u, 0x4140), 0x64806480u),
+                              hsub2(__byte_perm(u1, 0x64646464u, 0x4342), 0x64806480u));
+#pragma unroll
+                for (int half = 0; half < 2; half++) {
+                    const float2 dv = make_float2(d[2 * half], d[2 * half + 1]);
+                    const float2 q2 = make_float2(qsc[half][bb], qsc[half][bb]);
+                    s[i][half] = bb == 0 ? __fmul2_rn(dv, q2) : __ffma2_rn(dv, q2, s[i][half]);
+                }
+            }
+        }
+        bool grow = false;
+        bool on[4][2][2];
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+#pragma unroll
+            for (int half = 0; half < 2; half++) {
+                s[i][half] = __fmul2_rn(s[i][half], km[i]);
+                if (MASKED) {
+                    const int t = 8 * c4 + ((i + c4) & 3);
+                    on[i][half][0] = (win[half] >> t) & 1u;
+                    on[i][half][1] = (win[half] >> (t + 4)) & 1u;
+                    s[i][half].x = on[i][half][0] ? s[i][half].x : -INFINITY;
+                    s[i][half].y = on[i][half][1] ? s[i][half].y : -INFINITY;
+                }
+                grow |= fmaxf(s[i][half].x, s[i][half].y) > M[half] + TR_SLACK;
+            }
+        if (__any_sync(0xffffffffu, grow)) {
+            // rare: some row's maximum grew by a wide margin -> rescale its state
+#pragma unroll
+            for (int half = 0; half < 2; half++) {
+                float m = M[half];
+#pragma unroll
+                for (int i = 0; i < 4; i++) m = fmaxf(m, fmaxf(s[i][half].x, s[i][half].y));
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+                const float f = tr_ex2(M[half] - m);
+                M[half] = m;
+                sum[half] *= f;
+#pragma unroll
+                for (int cg = 0; cg < HD / 16; cg++)
+#pragma unroll
+                    for (int j = 0; j < 2; j++) {
+                        D[cg][j][2 * half] *= f;
+                        D[cg][j][2 * half + 1] *= f;
+                    }
+            }
+        }
+        // ---- weights: token pair i of row half -> A register (half + 2 (i % 2)) of
+        // k-step i / 2
+        uint32_t hi[2][4], lo[2][4];
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+#pragma unroll
+            for (int half = 0; half < 2; half++) {
+                const float2 y = __fadd2_rn(s[i][half], make_float2(-M[half], -M[half]));
+                const float2 p = make_float2(tr_ex2(y.x), tr_ex2(y.y));
+                sum[half] += p.x + p.y;
+                float2 w = __fmul2_rn(p, __fmul2_rn(vm[i], make_float2(vsc[half], vsc[half])));
+                if (MASKED) {  // a masked token's V step may be anything
+                    w.x = on[i][half][0] ? w.x : 0.0f;
+                    w.y = on[i][half][1] ? w.y : 0.0f;
+                }
+                const uint32_t wh = f2_to_h2(w.x, w.y);
+                hi[i >> 1][half + 2 * (i & 1)] = wh;
+                if (HILO) {
+                    const float2 back = h2_to_f2(wh);
+                    lo[i >> 1][half + 2 * (i & 1)] = f2_to_h2(w.x - back.x, w.y - back.y);
+                }
+            }
+        // ---- values: lane L gives the V row tok(L / 8, L % 8) of each 16-byte chunk
+        const int tv = 4 * (lane & 7) + (((lane >> 3) + ((lane & 7) >> 1)) & 3);
+        const uint32_t vrow = smem_u32(S.v[warp][st]) + (uint32_t)tv * HD;
+#pragma unroll
+        for (int cg = 0; cg < HD / 16; cg++) {
+            uint32_t r[4];
+            ldsm_x4_trans(vrow + ((uint32_t)(cg ^ (tv & 7)) << 4), r[0], r[1], r[2], r[3]);
+            uint32_t be[4], bo[4];
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const uint32_t u = r[j] ^ 0x80808080u;
+                be[j] = hsub2(__byte_perm(u, 0x64646464u, 0x4240), 0x64806480u);
+                bo[j] = hsub2(__byte_perm(u, 0x64646464u, 0x4341), 0x64806480u);
+            }
+#pragma unroll
+            for (int ks = 0; ks < 2; ks++) {
+                mma_f16_16816(D[cg][0], hi[ks], be[2 * ks], be[2 * ks + 1]);
+                mma_f16_16816(D[cg][1], hi[ks], bo[2 * ks], bo[2 * ks + 1]);
+                if (HILO) {
+                    mma_f16_16816(D[cg][0], lo[ks], be[2 * ks], be[2 * ks + 1]);
+                    mma_f16_16816(D[cg][1], lo[ks], bo[2 * ks], bo[2 * ks + 1]);
+                }
+            }
+        }
+    };
+
+    bool failed = false;
+    for (int i = 0; i < mine; i++) {
+        const int st = i % TR_STAGES, tile = first + TR_WARPS * i;
+        if ((i >> 5) != window) {
+            window = i >> 5;
+            page_cur = page_nxt;
+            page_nxt = load_window(window + 1);
+        }
+        const int32_t pg = page_of(i);
+        if (!__all_sync(0xffffffffu, mbar_wait_bounded(&S.bar[warp][st], (i / TR_STAGES) & 1))) {
+            // let the copies in flight land before leaving (bounded)
+            for (int j = i; j < mine && j < i + TR_STAGES; j++)
+                __all_sync(0xffffffffu, mbar_wait_bounded(&S.bar[warp][j % TR_STAGES],
+                                                          (j / TR_STAGES) & 1));
+            if (lane == 0) atomicOr(P.status, KQ8_STATUS_TIMEOUT);
+            failed = true;
+            break;
+        }
+        if (pg >= 0) {
+            if ((tile + 1) * TILE <= base)
+                step(st, tile, std::false_type{});
+            else
+                step(st, tile, std::true_type{});
+        }
+        __syncwarp();
+        if (i + TR_STAGES < mine) issue(i + TR_STAGES);
+    }
+
+    // ---- merge the warps (the V ring becomes [warp][16][HD] accumulators)
+    const bool cta_failed = __syncthreads_or(failed ? 1 : 0) != 0;
+    float* macc = reinterpret_cast<float*>(S.v);
+#pragma unroll
+    for (int half = 0; half < 2; half++) {
+        sum[half] += __shfl_xor_sync(0xffffffffu, sum[half], 1);
+        sum[half] += __shfl_xor_sync(0xffffffffu, sum[half], 2);
+        const float f = pow2i(ev[half]);
+        float* row = macc + (warp * TR_ROWS + gq + 8 * half) * HD;
+#pragma unroll
+        for (int cg = 0; cg < HD / 16; cg++)
+            *reinterpret_cast<float4*>(row + 16 * cg + 4 * c4) =
+                make_float4(D[cg][0][2 * half] * f, D[cg][1][2 * half] * f,
+                            D[cg][0][2 * half + 1] * f, D[cg][1][2 * half + 1] * f);
+        if (c4 == 0) S.ms[warp][gq + 8 * half] = make_float2(M[half], sum[half]);
+    }
+    __syncthreads();
+    const size_t pair = ((size_t)blockIdx.z * nkv + h) * P.row_tiles + rt;
+    auto out_at = [&](int r) -> size_t {
+        const int rr = rt * TR_ROWS + r;
+        return ((size_t)(q0 + rr / G) * P.nq + (size_t)h * G + rr % G) * HD + 4 * lane;
+    };
+    for (int r = warp; r < rows; r += TR_WARPS) {
+        float m = M_INIT, den = 0.0f;
+#pragma unroll
+        for (int w = 0; w < TR_WARPS; w++) m = fmaxf(m, S.ms[w][r].x);
+        float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int w = 0; w < TR_WARPS; w++) {
+            const float2 ms = S.ms[w][r];
+            const float f = tr_ex2(ms.x - m);
+            const float4 x = reinterpret_cast<const float4*>(macc + (w * TR_ROWS + r) * HD)[lane];
+            den += ms.y * f;
+            a.x += x.x * f;
+            a.y += x.y * f;
+            a.z += x.z * f;
+            a.w += x.w * f;
+        }
+        if (nch > 1) {
+            const size_t pr = (pair * TR_ROWS + r) * P.num_chunks + chunk;
+            reinterpret_cast<float4*>(P.part_acc + pr * HD)[lane] = a;
+            if (lane == 0) P.part_ms[pr] = make_float2(m, cta_failed ? -1.0f : den);
+        } else if (!cta_failed) {  // a row that sees no token gives 0
+            const float inv = den == 0.0f ? 0.0f : 1.0f;
+            const float dv = den == 0.0f ? 1.0f : den;
+            store_out4(P.out, P.dtype, out_at(r),
+                       make_float4(a.x / dv * inv, a.y / dv * inv, a.z / dv * inv, a.w / dv * inv));
+        }
+    }
+    if (nch == 1) return;
+
+    // ---- the last CTA of this (sequence, KV head, row tile) merges the chunks
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        __threadfence();
+        S.last = atomicAdd(&P.counters[pair], 1u) == (unsigned)(nch - 1);
+    }
+    __syncthreads();
+    if (!S.last) return;
+    __threadfence();
+    for (int r = warp; r < rows; r += TR_WARPS) {
+        const size_t at = (pair * TR_ROWS + r) * P.num_chunks;
+        float m = M_INIT, den = 0.0f;
+        float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        bool bad = false;
+#pragma unroll 8
+        for (int c = 0; c < nch; c++) {
+            const float2 ms = __ldcg(&P.part_ms[at + c]);
+            const float4 x =
+                __ldcg(reinterpret_cast<const float4*>(P.part_acc + (at + c) * HD) + lane);
+            bad |= ms.y < 0.0f;
+            const float mn = fmaxf(m, ms.x);
+            const float fo = tr_ex2(m - mn), fn = tr_ex2(ms.x - mn);
+            den = den * fo + ms.y * fn;
+            a.x = a.x * fo + x.x * fn;
+            a.y = a.y * fo + x.y * fn;
+            a.z = a.z * fo + x.z * fn;
+            a.w = a.w * fo + x.w * fn;
+            m = mn;
+        }
+        if (bad) continue;  // a timed-out chunk: the row stays as it was
+        const float inv = den == 0.0f ? 0.0f : 1.0f;
+        const float dv = den == 0.0f ? 1.0f : den;
+        store_out4(P.out, P.dtype, out_at(r),
+                   make_float4(a.x / dv * inv, a.y / dv * inv, a.z / dv * inv, a.w / dv * inv));
+    }
+    if (threadIdx.x == 0) P.counters[pair] = 0;  // ready for the next call
+}
+
+// A call's split: sequences per launch (so that the tickets of a launch fit the
+// header's counters), row tiles, chunks and the partials' places.
+struct TreePlan {
+    int seqs = 0, row_tiles = 1, chunk_tiles = TR_WARPS, num_chunks = 1;
+    size_t off_ms = 0, off_acc = 0, total = TR_HEADER;
+};
+TreePlan tree_plan(int B, int nq, int nkv, int max_seq_len, int max_q_len) {
+    TreePlan p;
+    const int64_t rows = (int64_t)max_q_len * (nq / nkv);
+    p.row_tiles = (int)((rows + TR_ROWS - 1) / TR_ROWS);
+    if (p.row_tiles < 1) p.row_tiles = 1;
+    const int64_t per_seq = (int64_t)nkv * p.row_tiles;
+    if (per_seq > (int64_t)TR_COUNTERS) return p;  // seqs = 0: unsupported
+    p.seqs = (int)((int64_t)TR_COUNTERS / per_seq);
+    if (p.seqs > B) p.seqs = B;
+    const int64_t pairs = (int64_t)p.seqs * per_seq;
+    const int64_t tiles = ((int64_t)max_seq_len + TILE - 1) / TILE;
+    // As the exact decode splits its lists: one wave of resident CTAs (3 per SM)
+    // where every list fits it with chunks of at most TR_MAX_CHUNK sub-tiles, at
+    // most 16 chunks a list; else about four waves, with long chunks, because a
+    // CTA streams nothing in its prologue and merge.  Chunks grow past
+    // TR_MAX_CHUNK only to keep the partials under 512 MB.
+    const int64_t slots = (int64_t)device_sms() * 3;
+    int64_t per = pairs > 0 ? slots / pairs : slots;
+    if (per > 16) per = 16;
+    int64_t c = per >= 1 && (tiles + per - 1) / per <= TR_MAX_CHUNK
+                    ? (tiles + per - 1) / per
+                    : (pairs * tiles + 4 * slots - 1) / (4 * slots);
+    if (c > TR_MAX_CHUNK) c = TR_MAX_CHUNK;
+    c = (c + TR_WARPS - 1) / TR_WARPS * TR_WARPS;
+    if (c < TR_WARPS) c = TR_WARPS;
+    constexpr int64_t PART = (int64_t)TR_ROWS * (HD * sizeof(float) + sizeof(float2));
+    while (c < tiles && pairs * ((tiles + c - 1) / c) * PART > (512ll << 20)) c *= 2;
+    p.chunk_tiles = (int)c;
+    p.num_chunks = tiles > 0 ? (int)((tiles + c - 1) / c) : 1;
+    auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+    const size_t parts = (size_t)pairs * TR_ROWS * p.num_chunks;
+    p.off_ms = TR_HEADER;
+    p.off_acc = up(p.off_ms + parts * sizeof(float2));
+    p.total = up(p.off_acc + parts * HD * sizeof(float));
+    return p;
+}
+
+constexpr size_t TR_SMEM = sizeof(TreeSmem) + 1024;  // slack to round the base up
+
+template <bool HILO>
+int launch_tree(const TreeParams& p, dim3 grid, cudaStream_t s) {
+    if (cudaFuncSetAttribute(kq8_tree_kernel<HILO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)TR_SMEM) != cudaSuccess)
+        return KQ8_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(TR_THREADS);
+    cfg.dynamicSmemBytes = TR_SMEM;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kq8_tree_kernel<HILO>, p) != cudaSuccess) return KQ8_ERR_CUDA;
+    return cudaPeekAtLastError() == cudaSuccess ? KQ8_OK : KQ8_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace kq8
+
+using namespace kq8;
+
+extern "C" {
+
+size_t kq8_tree_workspace_bytes(int32_t B, int32_t nq, int32_t nkv, int32_t max_seq_len,
+                                int32_t max_q_len) {
+    if (B < 0 || nq < 1 || nkv < 1 || nq % nkv || max_seq_len < 0 || max_q_len < 0) return 0;
+    return tree_plan(B, nq, nkv, max_seq_len, max_q_len).total;
+}
+
+int kq8_tree_attn(void* out, const void* q, int32_t dtype, size_t q_token_stride,
+                  size_t q_head_stride, int32_t total_q, const kq8_cache_t* cache,
+                  const int32_t* page_table, int32_t max_pages, const int32_t* seq_lens,
+                  const int32_t* q_offsets, const uint32_t* tree_mask, int32_t mask_words,
+                  int32_t max_seq_len, int32_t max_q_len, int32_t B, int32_t nq, float scale,
+                  void* workspace, size_t workspace_bytes, kq8_stream_t stream) {
+    int rc = check_cache_args(cache);
+    if (rc) return rc;
+    if (dtype != KQ8_F32 && dtype != KQ8_F16 && dtype != KQ8_BF16) return KQ8_ERR_UNSUPPORTED;
+    if (B < 0 || nq < 1 || total_q < 0 || max_seq_len < 0 || max_q_len < 0 || max_pages < 0 ||
+        mask_words < 0)
+        return KQ8_ERR_INVALID_ARG;
+    const int nkv = cache->num_kv_heads;
+    if (nq % nkv != 0 || nq / nkv > MAX_G) return KQ8_ERR_UNSUPPORTED;
+    if ((int64_t)max_seq_len > (int64_t)max_pages * cache->kv_bs) return KQ8_ERR_INVALID_ARG;
+    if (max_q_len > max_seq_len) return KQ8_ERR_INVALID_ARG;
+    if (max_seq_len >= (1 << 29) || B > 65535 || nkv > 65535 || max_q_len > KQ8_TREE_MAX_NODES)
+        return KQ8_ERR_UNSUPPORTED;
+    if (tree_mask && (int64_t)mask_words * 32 < max_q_len) return KQ8_ERR_INVALID_ARG;
+    const TreePlan plan = tree_plan(B, nq, nkv, max_seq_len, max_q_len);
+    if (!workspace || (uintptr_t)workspace % 256 != 0 || workspace_bytes < plan.total)
+        return KQ8_ERR_WORKSPACE;
+    if (B == 0 || max_q_len == 0) return KQ8_OK;
+    if (plan.seqs < 1) return KQ8_ERR_UNSUPPORTED;
+    if (!out || !q || !seq_lens || !q_offsets || !page_table) return KQ8_ERR_INVALID_ARG;
+    // a lane reads 4 elements of a q row and writes 4 of an output row
+    const size_t quad = dtype == KQ8_F32 ? 16 : 8;
+    if ((uintptr_t)out % quad || (uintptr_t)q % quad || q_token_stride % 4 || q_head_stride % 4 ||
+        q_token_stride > MAX_STRIDE || q_head_stride > MAX_STRIDE ||
+        (tree_mask && (uintptr_t)tree_mask % 4))
+        return KQ8_ERR_INVALID_ARG;
+    TreeParams p;
+    std::memset(&p, 0, sizeof(p));
+    rc = encode_vmap(&p.vmap, *cache, false);
+    if (rc) return rc;
+    p.out = out;
+    p.q = q;
+    p.q_st = (int64_t)q_token_stride;
+    p.q_sh = (int64_t)q_head_stride;
+    p.dtype = dtype;
+    p.total_q = total_q;
+    p.cache = *cache;
+    p.page_table = page_table;
+    p.max_pages = max_pages;
+    p.seq_lens = seq_lens;
+    p.q_off = q_offsets;
+    p.mask = tree_mask;
+    p.mask_words = mask_words;
+    p.max_seq_len = max_seq_len;
+    p.max_q_len = max_q_len;
+    p.nq = nq;
+    p.G = nq / nkv;
+    p.scale = scale;
+    p.chunk_tiles = plan.chunk_tiles;
+    p.num_chunks = plan.num_chunks;
+    p.row_tiles = plan.row_tiles;
+    char* ws = static_cast<char*>(workspace);
+    p.part_ms = reinterpret_cast<float2*>(ws + plan.off_ms);
+    p.part_acc = reinterpret_cast<float*>(ws + plan.off_acc);
+    p.status = reinterpret_cast<uint32_t*>(ws);
+    p.counters = reinterpret_cast<uint32_t*>(ws + TR_STATUS_BYTES);
+    for (p.b0 = 0; p.b0 < B; p.b0 += plan.seqs) {
+        const int seqs = B - p.b0 < plan.seqs ? B - p.b0 : plan.seqs;
+        const dim3 grid((unsigned)(plan.num_chunks * plan.row_tiles), (unsigned)nkv, (unsigned)seqs);
+        rc = dtype == KQ8_BF16 ? launch_tree<false>(p, grid, (cudaStream_t)stream)
+                               : launch_tree<true>(p, grid, (cudaStream_t)stream);
+        if (rc) return rc;
+    }
+    return KQ8_OK;
+}
+
+}  // extern "C"

@@ -38,6 +38,10 @@ KQ8_STATUS_BAD_SLOT = 0x4
 KQ8_STATUS_TIMEOUT = 0x8
 
 HEAD_DIM = 128
+TREE_MAX_NODES = 1024
+
+# element types of the calls that take one (KQ8_F32, KQ8_F16, KQ8_BF16)
+DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 
 
 class kq8_cache_t(ctypes.Structure):
@@ -90,6 +94,13 @@ _lib.kq8_decode_attn_q4.argtypes = [_P, _P, _CP, _P, _I32, _P, _I32, _I32, _I32,
                                     _P, _SZ, _P]
 _lib.kq8_sparse_decode_attn_shared.argtypes = [_P, _P, _CP, _P, _I32, _P, _I32, _I32, _I32,
                                                ctypes.c_float, _I32, _I32, _I32, _P, _P, _SZ, _P]
+_lib.kq8_write_kv.argtypes = [_CP, _I32, _P, _P, _I32, _SZ, _SZ, _SZ, _SZ, _P, _I32, _P, _P]
+_lib.kq8_read_kv.argtypes = [_CP, _I32, _P, _P, _I32, _SZ, _SZ, _SZ, _SZ, _P, _I32, _P, _P]
+_lib.kq8_tree_workspace_bytes.argtypes = [_I32, _I32, _I32, _I32, _I32]
+_lib.kq8_tree_workspace_bytes.restype = _SZ
+_lib.kq8_tree_attn.argtypes = [_P, _P, _I32, _SZ, _SZ, _I32, _CP, _P, _I32, _P, _P, _P, _I32,
+                               _I32, _I32, _I32, _I32, ctypes.c_float, _P, _SZ, _P]
+_lib.kq8_tree_commit.argtypes = [_CP, _I32, _P, _I32, _P, _P, _P, _I32, _I32, _P, _P]
 _lib.kq8_read_status.argtypes = [_P, ctypes.POINTER(ctypes.c_uint32), _P]
 _lib.kq8_strerror.argtypes = [ctypes.c_int]
 _lib.kq8_strerror.restype = ctypes.c_char_p
@@ -506,6 +517,122 @@ def kq8_read_status(word: torch.Tensor, stream=None) -> int:
     st = ctypes.c_uint32(0)
     _check(_lib.kq8_read_status(_ptr(word), ctypes.byref(st), _stream(stream)), "kq8_read_status")
     return int(st.value)
+
+
+# ---- rows of any type and stride, draft trees ----
+
+def _rows(t: torch.Tensor, name: str) -> ctypes.c_void_p:
+    """Pointer of a [tokens, heads, 128] tensor whose rows are adjacent elements."""
+    if not t.is_cuda:
+        raise ValueError("kq8 takes CUDA tensors")
+    if t.dtype not in DTYPES:
+        raise TypeError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
+    if t.dim() != 3 or t.shape[2] != HEAD_DIM or t.stride(2) != 1:
+        raise ValueError(f"{name} must be [tokens, heads, 128] with adjacent elements in a row")
+    return t.data_ptr()
+
+
+def _stream_on(device: torch.device, stream, *tensors) -> ctypes.c_void_p:
+    """The stream of a call on `device`: the given one, or that device's current
+    one.  Every tensor of the call has to be there, and the device has to be the
+    current one (a launch goes to the current device)."""
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"the call's tensors are on {device} and {t.device}")
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"the call's tensors are on {device}, not on the current device")
+    return _stream(stream)
+
+
+def _rows_args(cache, k, v, slot, status, stream):
+    kp, vp = _rows(k, "k"), _rows(v, "v")
+    _dtype(slot, torch.int32, "slot")
+    T, nkv = slot.numel(), cache.num_kv_heads
+    if tuple(k.shape) != (T, nkv, HEAD_DIM) or v.shape != k.shape or v.dtype != k.dtype:
+        raise ValueError("k and v must be [len(slot), nkv, 128] of one type")
+    if status is not None:
+        _dtype(status, torch.int32, "status")
+    st = _stream_on(cache.k.device, stream, k, v, slot, status)
+    sk, sv = k.stride(), v.stride()
+    return (ctypes.byref(cache.struct), cache.bits, kp, vp, DTYPES[k.dtype], sk[0], sk[1], sv[0],
+            sv[1], _ptr(slot), T, _ptr(status), st)
+
+
+def kq8_write_kv(cache: PagedKVCache, k: torch.Tensor, v: torch.Tensor, slot: torch.Tensor,
+                 status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Write path for k, v [T, nkv, 128] of float32, float16 or bfloat16 with any
+    token and head stride, into a q8 or q4 cache; slot int32 [T]
+    (include/kq8.h)."""
+    _check(_lib.kq8_write_kv(*_rows_args(cache, k, v, slot, status, stream)), "kq8_write_kv")
+
+
+def kq8_read_kv(cache: PagedKVCache, k: torch.Tensor, v: torch.Tensor, slot: torch.Tensor,
+                status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """The values of the cache's rows at slot int32 [T] into k, v [T, nkv, 128] of
+    float32, float16 or bfloat16, any strides; rows with a negative slot stay as
+    they were (include/kq8.h)."""
+    _check(_lib.kq8_read_kv(*_rows_args(cache, k, v, slot, status, stream)), "kq8_read_kv")
+
+
+def kq8_tree_workspace_bytes(B: int, nq: int, nkv: int, max_seq_len: int, max_q_len: int) -> int:
+    return int(_lib.kq8_tree_workspace_bytes(B, nq, nkv, max_seq_len, max_q_len))
+
+
+def kq8_tree_attn(out: torch.Tensor, q: torch.Tensor, cache: PagedKVCache,
+                  page_table: torch.Tensor, seq_lens: torch.Tensor, q_offsets: torch.Tensor,
+                  tree_mask: Optional[torch.Tensor], max_seq_len: int, max_q_len: int,
+                  scale: float, workspace: torch.Tensor, stream=None) -> None:
+    """Attention of drafted tokens over a q8 cache (include/kq8.h): q and out
+    [total_q, nq, 128] of float32, float16 or bfloat16, packed by sequence per
+    q_offsets [B+1]; seq_lens counts the drafts; tree_mask int32 [total_q,
+    mask_words] holds each node's visible nodes as bits (None: a chain)."""
+    if cache.bits != 8:
+        raise ValueError("the tree attention reads a q8 cache")
+    qp = _rows(q, "q")
+    _dtype(out, q.dtype, "out")
+    _dtype(page_table, torch.int32, "page_table")
+    _dtype(seq_lens, torch.int32, "seq_lens")
+    _dtype(q_offsets, torch.int32, "q_offsets")
+    if out.shape != q.shape:
+        raise ValueError("q and out must be [total_q, nq, 128]")
+    B = seq_lens.numel()
+    if q_offsets.numel() != B + 1 or page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError("q_offsets must be [B+1] and page_table [B, max_pages]")
+    words = 0
+    if tree_mask is not None:
+        _dtype(tree_mask, torch.int32, "tree_mask")
+        if tree_mask.dim() != 2 or tree_mask.shape[0] != q.shape[0]:
+            raise ValueError("tree_mask must be [total_q, mask_words]")
+        words = tree_mask.shape[1]
+    st = _stream_on(cache.k.device, stream, out, q, page_table, seq_lens, q_offsets, tree_mask,
+                    workspace)
+    _check(_lib.kq8_tree_attn(_ptr(out), qp, DTYPES[q.dtype], q.stride(0), q.stride(1), q.shape[0],
+                              ctypes.byref(cache.struct), _ptr(page_table), page_table.shape[1],
+                              _ptr(seq_lens), _ptr(q_offsets), _ptr(tree_mask), words,
+                              int(max_seq_len), int(max_q_len), B, q.shape[1], float(scale),
+                              _ptr(workspace), workspace.numel() * workspace.element_size(), st),
+           "kq8_tree_attn")
+
+
+def kq8_tree_commit(cache: PagedKVCache, page_table: torch.Tensor, base_lens: torch.Tensor,
+                    path: torch.Tensor, path_len: torch.Tensor,
+                    status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Moves each sequence's accepted drafts path int32 [B, max_path] (the first
+    path_len[b] of a row, ascending) behind its base_lens[b] committed tokens
+    (include/kq8.h)."""
+    for t, name in ((page_table, "page_table"), (base_lens, "base_lens"), (path, "path"),
+                    (path_len, "path_len")):
+        _dtype(t, torch.int32, name)
+    B = base_lens.numel()
+    if (path.dim() != 2 or path.shape[0] != B or path_len.numel() != B
+            or page_table.dim() != 2 or page_table.shape[0] != B):
+        raise ValueError("page_table must be [B, max_pages], path [B, max_path], path_len [B]")
+    if status is not None:
+        _dtype(status, torch.int32, "status")
+    st = _stream_on(cache.k.device, stream, page_table, base_lens, path, path_len, status)
+    _check(_lib.kq8_tree_commit(ctypes.byref(cache.struct), cache.bits, _ptr(page_table),
+                                page_table.shape[1], _ptr(base_lens), _ptr(path), _ptr(path_len),
+                                path.shape[1], B, _ptr(status), st), "kq8_tree_commit")
 
 
 # ---- test-only exports -------------------------------------------------------

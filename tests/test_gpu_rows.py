@@ -1,0 +1,285 @@
+"""Cache rows in and out through the public calls: kq8_write_kv (fp32, fp16 and
+bf16 rows of any stride, q8 and q4), kq8_read_kv and kq8_tree_commit, against the
+write rule computed in the test and against kq8_append_kv.
+
+Codes and maxima are compared for equality: they are IEEE fp32 operations, which
+numpy performs alike.  A value read back is code * fl(m * fl(1/127)), again fp32
+operations, then one rounding to the type (torch's conversion): equality too."""
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA GPU", allow_module_level=True)
+
+from query_decode_attention_gb300 import kq8, paged  # noqa: E402
+
+DEV = "cuda:0"
+TYPES = [torch.float32, torch.float16, torch.bfloat16]
+
+
+def _rule(x, bits):
+    """(codes, stored maxima) of fp32 rows [..., 128] by article 9-3 §2."""
+    top = np.float32(127 if bits == 8 else 7)
+    x = x.astype(np.float32)
+    m = np.abs(x).max(-1)
+    d = (m * (np.float32(1) / top)).astype(np.float32)[..., None]
+    with np.errstate(invalid="ignore", divide="ignore"):
+        y = (x / d).astype(np.float32).astype(np.float64)
+    c = np.sign(y) * np.floor(np.abs(y) + 0.5)
+    c = np.where(m[..., None] == 0, 0.0, np.clip(np.nan_to_num(c), -top, top))
+    return c.astype(np.int8), m
+
+
+def _unpack(cache, slots):
+    return (paged.unpack if cache.bits == 8 else paged.unpack_q4)(cache, slots)
+
+
+def _filled(pages, nkv, kv_bs, bits, seed=0):
+    """A cache whose every byte holds something, to see what a call leaves alone."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    c = kq8.PagedKVCache(pages, nkv, kv_bs, DEV, bits=bits)
+    if bits == 8:
+        c.k.copy_(torch.randint(-127, 128, c.k.shape, generator=g, device=DEV))
+        c.v.copy_(torch.randint(-127, 128, c.v.shape, generator=g, device=DEV))
+    else:
+        for t in (c.k, c.v):
+            t.copy_((torch.randint(1, 16, t.shape, generator=g, device=DEV)
+                     + 16 * torch.randint(1, 16, t.shape, generator=g, device=DEV))
+                    .to(torch.uint8).view(torch.int8))
+    c.kscale.uniform_(0.5, 4.0, generator=g)
+    c.vscale.uniform_(0.5, 4.0, generator=g)
+    return c
+
+
+def _clone(c):
+    return kq8.PagedKVCache(c.num_pages, c.num_kv_heads, c.kv_bs, k=c.k.clone(), v=c.v.clone(),
+                            kscale=c.kscale.clone(), vscale=c.vscale.clone(), bits=c.bits)
+
+
+def _same(a, b):
+    return (torch.equal(a.k, b.k) and torch.equal(a.v, b.v) and torch.equal(a.kscale, b.kscale)
+            and torch.equal(a.vscale, b.vscale))
+
+
+def _strided(shape, dtype, layout, seed):
+    """A [T, nkv, 128] view of `layout` filled with normal values of spread e^N(0, 2)."""
+    T, nkv, _ = shape
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    if layout == "packed":
+        t = torch.empty((T, nkv, 128), dtype=dtype, device=DEV)
+    elif layout == "fused":      # a slice of a [T, 3 nkv + 1, 128] projection
+        t = torch.full((T, 3 * nkv + 1, 128), float("nan"), dtype=dtype, device=DEV)[:, nkv:2 * nkv]
+    elif layout == "heads":      # head-major
+        t = torch.empty((nkv, T, 128), dtype=dtype, device=DEV).transpose(0, 1)
+    else:                        # "odd": rows 2 bytes off the 16-byte grid
+        t = torch.full((T, nkv * 131 + 1), float("nan"), dtype=dtype, device=DEV)[:, 1:]
+        t = t.unflatten(1, (nkv, 131))[..., :128]
+    x = torch.randn(shape, generator=g, device=DEV) * torch.exp(
+        2 * torch.randn((T, nkv, 1), generator=g, device=DEV))
+    t.copy_(x)
+    return t
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("layout", ["packed", "fused", "heads", "odd"])
+@pytest.mark.parametrize("T,nkv,kv_bs", [(1, 1, 32), (33, 3, 64), (500, 8, 32), (97, 2, 256)])
+def test_write_then_read(bits, dtype, layout, T, nkv, kv_bs):
+    pages = -(-T // kv_bs) + 2
+    cache = _filled(pages, nkv, kv_bs, bits)
+    k, v = (_strided((T, nkv, 128), dtype, layout, s) for s in (1, 2))
+    slots = np.random.default_rng(T).permutation(pages * kv_bs)[:T].astype(np.int32)
+    if T == 97:
+        slots = np.arange(T, dtype=np.int32) + kv_bs - 5  # consecutive, across a page's end
+    st = torch.tensor(slots, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    before = _clone(cache)
+    kq8.kq8_write_kv(cache, k, v, st, status)
+    kc, km, vc, vm = _unpack(cache, slots)
+    for x, c, m in ((k, kc, km), (v, vc, vm)):
+        c_ref, m_ref = _rule(x.float().cpu().numpy(), bits)
+        assert np.array_equal(m, m_ref)
+        assert np.array_equal(c, c_ref)
+    # rows of other slots untouched: writing the old rows back restores the cache
+    other = np.setdiff1d(np.arange(pages * kv_bs), slots)
+    for a, b in zip(_unpack(cache, other), _unpack(before, other)):
+        assert np.array_equal(a, b)
+    # read into the same layouts
+    ko, vo = (_strided((T, nkv, 128), dtype, layout, s) for s in (3, 4))
+    kq8.kq8_read_kv(cache, ko, vo, st, status)
+    inv = np.float32(1) / np.float32(127 if bits == 8 else 7)
+    for o, c, m in ((ko, kc, km), (vo, vc, vm)):
+        val = c.astype(np.float32) * (m * inv).astype(np.float32)[..., None]
+        assert torch.equal(o.cpu(), torch.tensor(val).to(dtype))
+    assert int(status.item()) == 0
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+def test_write_equals_append(bits):
+    T, nkv = 300, 4
+    k, v = (_strided((T, nkv, 128), torch.float32, "packed", s) for s in (1, 2))
+    k[7] = 0.0
+    k[8] *= 1e-42 / k[8].abs().amax()  # subnormal rows
+    v[9] *= 3e38 / v[9].abs().amax()
+    k[10, 1, 5] = float("inf")
+    v[11, 2, 6] = float("nan")
+    a, b = _filled(20, nkv, 32, bits), _filled(20, nkv, 32, bits)
+    slot = torch.arange(T, dtype=torch.int32, device=DEV) + 3
+    (kq8.kq8_append_kv if bits == 8 else kq8.kq8_append_kv_q4)(a, k, v, slot)
+    kq8.kq8_write_kv(b, k, v, slot)
+    assert _same(a, b)
+
+
+def test_skipped_and_bad_slots_leave_rows_alone():
+    T, nkv = 40, 2
+    cache = _filled(3, nkv, 32, 8)
+    k, v = (_strided((T, nkv, 128), torch.bfloat16, "fused", s) for s in (1, 2))
+    slots = np.arange(T, dtype=np.int32)
+    slots[[3, 5]] = -1
+    slots[7] = 3 * 32          # one past the pool
+    slots[9] = 2 ** 31 - 1
+    ok = np.setdiff1d(np.arange(T), [3, 5, 7, 9])
+    before = _clone(cache)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    kq8.kq8_write_kv(cache, k, v, torch.tensor(slots, device=DEV), status)
+    assert kq8.kq8_read_status(status) == kq8.KQ8_STATUS_BAD_SLOT
+    ref = _clone(before)
+    kq8.kq8_write_kv(ref, k[ok], v[ok], torch.tensor(slots[ok], device=DEV))
+    assert _same(cache, ref)
+    ko, vo = (torch.full((T, nkv, 128), 7.0, dtype=torch.float16, device=DEV) for _ in range(2))
+    kq8.kq8_read_kv(cache, ko, vo, torch.tensor(slots, device=DEV), status)
+    assert kq8.kq8_read_status(status) == kq8.KQ8_STATUS_BAD_SLOT
+    assert bool((ko[[3, 5, 7, 9]] == 7).all()) and bool((vo[[3, 5, 7, 9]] == 7).all())
+    kq8.kq8_write_kv(cache, k, v, torch.tensor(slots, device=DEV))  # no status word: still skipped
+    assert _same(cache, ref)
+
+
+def test_no_tokens():
+    cache = _filled(2, 2, 32, 8)
+    before = _clone(cache)
+    e = torch.empty((0, 2, 128), dtype=torch.bfloat16, device=DEV)
+    s = torch.empty(0, dtype=torch.int32, device=DEV)
+    kq8.kq8_write_kv(cache, e, e, s)
+    kq8.kq8_read_kv(cache, e, e, s)
+    assert _same(cache, before)
+
+
+def test_read_twice_and_slots_past_2_gib():
+    # a pool whose K array passes 2^31 bytes: 2^31 / (8 * 32 * 128) = 65536 pages
+    nkv, kv_bs, pages = 8, 32, 65600
+    cache = kq8.PagedKVCache(pages, nkv, kv_bs, DEV)
+    T = 70
+    slot = torch.arange(pages * kv_bs - T, pages * kv_bs, dtype=torch.int32, device=DEV)
+    k, v = (_strided((T, nkv, 128), torch.bfloat16, "packed", s) for s in (1, 2))
+    kq8.kq8_write_kv(cache, k, v, slot)
+    outs = [torch.empty_like(k) for _ in range(4)]
+    twice = torch.cat([slot[:35], slot[:35]])      # a slot read twice
+    kq8.kq8_read_kv(cache, outs[0], outs[1], slot)
+    kq8.kq8_read_kv(cache, outs[2], outs[3], twice)
+    assert torch.equal(outs[2][:35], outs[0][:35]) and torch.equal(outs[2][35:], outs[0][:35])
+    assert torch.equal(outs[3][35:], outs[1][:35])
+    c, m = _rule(k.float().cpu().numpy(), 8)
+    val = c.astype(np.float32) * (m * (np.float32(1) / np.float32(127)))[..., None]
+    assert torch.equal(outs[0].cpu(), torch.tensor(val).to(torch.bfloat16))
+
+
+# ---------------------------------------------------------------------------
+# kq8_tree_commit
+# ---------------------------------------------------------------------------
+def _committed(cache, table, base, paths):
+    """The cache after every path is moved, rows read before any is written."""
+    ref = _clone(cache)
+    for b, path in enumerate(paths):
+        src = [int(table[b][(base[b] + j) // cache.kv_bs]) * cache.kv_bs + (base[b] + j) % cache.kv_bs
+               for j in path]
+        dst = [int(table[b][(base[b] + i) // cache.kv_bs]) * cache.kv_bs + (base[b] + i) % cache.kv_bs
+               for i in range(len(path))]
+        for s, d in zip(src, dst):
+            ps, rs, pd, rd = s // cache.kv_bs, s % cache.kv_bs, d // cache.kv_bs, d % cache.kv_bs
+            at = lambda r: r % 32 % 4 * 8 + r % 32 // 4  # noqa: E731
+            ref.k[pd, :, rd // 32, :, at(rd)] = cache.k[ps, :, rs // 32, :, at(rs)]
+            ref.v[pd, :, rd] = cache.v[ps, :, rs]
+            ref.kscale[pd, :, rd] = cache.kscale[ps, :, rs]
+            ref.vscale[pd, :, rd] = cache.vscale[ps, :, rs]
+    return ref
+
+
+def _ints(x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+@pytest.mark.parametrize("bits,kv_bs,nkv", [(8, 32, 8), (4, 64, 3), (8, 256, 1)])
+def test_commit(bits, kv_bs, nkv):
+    rng = np.random.default_rng(kv_bs + bits)
+    # overlapping moves, one longer than a batch, the identity, nothing, a page's end
+    paths = [[0, 2, 3, 7], sorted(rng.choice(90, 50, replace=False).tolist()), list(range(6)), [],
+             [5], [1, 2, 3, 4, 5, 6, 7, 8]]
+    base = [0, 37, 3, 10, kv_bs - 2, kv_bs - 4]
+    depth = max(len(p) for p in paths)
+    max_pages = -(-(37 + 90) // kv_bs) + 1
+    table = rng.permutation(len(paths) * max_pages + 1)[:len(paths) * max_pages].reshape(-1, max_pages)
+    cache = _filled(len(paths) * max_pages + 1, nkv, kv_bs, bits)
+    ref = _committed(cache, table, base, paths)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    # entries behind a path's end are not looked at
+    kq8.kq8_tree_commit(cache, _ints(table), _ints(base),
+                        _ints([p + [-9] * (depth - len(p)) for p in paths]),
+                        _ints([len(p) for p in paths]), status)
+    assert kq8.kq8_read_status(status) == 0
+    assert _same(cache, ref)
+
+
+@pytest.mark.parametrize("path,n,base,table,bit", [
+    ([0, 2, 2], 3, 5, [0, 1], "BAD_SEQLEN"),       # not ascending
+    ([3, 1], 2, 5, [0, 1], "BAD_SEQLEN"),
+    ([-1, 4], 2, 5, [0, 1], "BAD_SEQLEN"),
+    ([1, 2], 3, 5, [0, 1], "BAD_SEQLEN"),          # longer than max_path
+    ([1, 2], -1, 5, [0, 1], "BAD_SEQLEN"),
+    ([1, 2], 2, -1, [0, 1], "BAD_SEQLEN"),
+    ([1, 60], 2, 5, [0, 1], "BAD_SEQLEN"),         # position 65 of 64
+    ([1, 2 ** 31 - 1], 2, 5, [0, 1], "BAD_SEQLEN"),
+    ([1, 30], 2, 5, [0, 4], "BAD_PAGE"),           # one past the pool
+    ([1, 30], 2, 5, [0, -1], "BAD_PAGE"),
+])
+def test_bad_path_moves_nothing(path, n, base, table, bit):
+    cache = _filled(4, 2, 32, 8)
+    # sequence 1 is sound and moves all the same
+    good = _committed(cache, [table, [2, 3]], [0, 30], [[], [1, 3]])
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    pad = path + [0] * (3 - len(path)) if n != 3 else path
+    width = max(len(pad), 2)
+    kq8.kq8_tree_commit(cache, _ints([table, [2, 3]]), _ints([base, 30]),
+                        _ints([pad, [1, 3] + [0] * (width - 2)]), _ints([n, 2]), status)
+    assert kq8.kq8_read_status(status) == getattr(kq8, "KQ8_STATUS_" + bit)
+    assert _same(cache, good)
+
+
+def test_write_read_commit_on_a_side_stream_and_in_a_graph():
+    T, nkv = 64, 2
+    k, v = (_strided((T, nkv, 128), torch.bfloat16, "fused", s) for s in (1, 2))
+    a, b = _filled(4, nkv, 32, 8), _filled(4, nkv, 32, 8)
+    slot = torch.arange(T, dtype=torch.int32, device=DEV)
+    table, base, path, plen = _ints([[0, 1, 2, 3]]), _ints([8]), _ints([[0, 3, 9]]), _ints([3])
+    outs = [torch.zeros((T, nkv, 128), device=DEV) for _ in range(4)]
+
+    def step(c, ko, vo):
+        kq8.kq8_write_kv(c, k, v, slot)
+        kq8.kq8_tree_commit(c, table, base, path, plen)
+        kq8.kq8_read_kv(c, ko, vo, slot)
+    step(a, outs[0], outs[1])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            step(b, outs[2], outs[3])
+        for _ in range(3):  # every replay writes the rows anew
+            g.replay()
+    torch.cuda.synchronize()
+    assert _same(a, b)
+    assert torch.equal(outs[0], outs[2]) and torch.equal(outs[1], outs[3])
