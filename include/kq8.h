@@ -19,8 +19,8 @@
  *     nothing and keeps no state between calls.
  *   - Calls enqueue work on `stream` (a cudaStream_t; NULL = the legacy default
  *     stream) and return without waiting for it.  Stream order holds as for
- *     ordinary launches.  The decode kernels, the tree attention and the calls
- *     that write, read or move cache rows are programmatic
+ *     ordinary launches.  The decode kernels, the tree and the prompt attention
+ *     and the calls that write, read or move cache rows are programmatic
  *     launches (cudaLaunchAttributeProgrammaticStreamSerialization): one of
  *     them may be scheduled while the kernel just before it on the stream
  *     finishes (this library's, or any code's that signals its dependents
@@ -481,6 +481,36 @@ int kq8_tree_commit(const kq8_cache_t* cache, int32_t bits, const int32_t* page_
                     int32_t max_pages, const int32_t* base_lens, const int32_t* path,
                     const int32_t* path_len, int32_t max_path, int32_t B, uint32_t* status,
                     kq8_stream_t stream);
+
+/*
+ * Causal attention over packed prompts from their own queries, keys and values (a
+ * prompt's first pass: no cache is read, so nothing is quantised):
+ *   out[i][h] = sum_j softmax_j(scale * q[i][h] . k[j][h / G]) * v[j][h / G]
+ * over the tokens j <= i of i's own sequence.
+ *   out         : dtype [total][nq][128] (device), contiguous, 16-byte aligned.
+ *   q           : dtype [total][nq][128] with strides of its tokens and heads in
+ *                 elements, k and v likewise [total][nkv][128]; the 128 elements of a
+ *                 row adjacent, pointers 16-byte aligned, strides multiples of 8.
+ *   dtype       : KQ8_F16 or KQ8_BF16, of all four.  Scores, maxima and sums are fp32;
+ *                 the softmax weights enter the value product rounded to dtype, and
+ *                 outputs are rounded once.
+ *   cu_seqlens  : int32 [B+1] (device): sequence b is rows cu_seqlens[b] ..
+ *                 cu_seqlens[b+1] - 1.  Rows outside every sequence stay as they were
+ *                 and are not looked at.
+ *   max_len     : host bound on a sequence's length (grid size).
+ *   nq, nkv     : nq % nkv == 0, G = nq / nkv in 1..8; scale > 0 and finite.
+ *   status      : optional uint32 word (device).  A sequence that is longer than
+ *                 max_len, descends or leaves total sets KQ8_STATUS_BAD_SEQLEN and is
+ *                 skipped.
+ * A k row that is not finite reaches the rows at and behind it; a v row that is not
+ * finite may also reach up to 127 rows before it; never another sequence.  Runs on
+ * the tcgen05 tensor cores.
+ */
+int kq8_prompt_attn(void* out, const void* q, const void* k, const void* v, int32_t dtype,
+                    size_t q_token_stride, size_t q_head_stride, size_t k_token_stride,
+                    size_t k_head_stride, size_t v_token_stride, size_t v_head_stride,
+                    const int32_t* cu_seqlens, int32_t total, int32_t max_len, int32_t B,
+                    int32_t nq, int32_t nkv, float scale, uint32_t* status, kq8_stream_t stream);
 
 /*
  * Copies the status word of `workspace` (or of a kq8_append_kv status word) to

@@ -52,6 +52,18 @@ __device__ __forceinline__ uint64_t sdesc(uint32_t saddr, uint32_t lbo, uint32_t
            ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46);
 }
 
+// The same for rows of 128 bytes laid out with the 128-byte swizzle (as TMA
+// stores them), groups of eight rows 1024 B.  K-major: sbo is the distance
+// between groups along M (or N), lbo unused.  MN-major (B: IDESC_B_MN): a row
+// holds 64 elements along N, lbo is the distance between such panels along N,
+// sbo the distance between groups of eight rows along K.  Layout 2 in bits
+// 61-63; operands start on 1024 bytes.
+__device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+    return sdesc(saddr, lbo, sbo) | (2ull << 61);
+}
+// Instruction descriptor bit 16: B is MN-major.
+constexpr uint32_t IDESC_B_MN = 1u << 16;
+
 // Instruction descriptor of kind::f16 with an fp32 accumulator, both operands
 // K-major: D format in bits 4-5 (1 = f32), A and B formats in bits 7-9 and
 // 10-12 (0 = f16, 1 = bf16), N >> 3 in bits 17-22, M >> 4 in bits 24-28.
@@ -71,6 +83,16 @@ __device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a_desc, uint64
         "{ .reg .pred p; setp.ne.b32 p, %4, 0;"
         " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d_tmem),
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
+}
+// The same with A in tensor memory: row i in lane i, two 16-bit elements of K
+// per 32-bit column.
+__device__ __forceinline__ void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                           uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{ .reg .pred p; setp.ne.b32 p, %4, 0;"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate)
         : "memory");
 }
 // Arrive once on `bar` when every MMA this thread issued so far has completed.
@@ -114,6 +136,32 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&r)[16]) {
           "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
         : "r"(taddr)
         : "memory");
+}
+// 32 lanes x 32 columns without the wait: the registers hold the data after a
+// wait (tmem_ld128 below).
+__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, float* r) {
+    uint32_t* u = reinterpret_cast<uint32_t*>(r);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
+        "%28, %29, %30, %31}, [%32];"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]),
+          "=r"(u[7]), "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]),
+          "=r"(u[13]), "=r"(u[14]), "=r"(u[15]), "=r"(u[16]), "=r"(u[17]), "=r"(u[18]),
+          "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]),
+          "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]),
+          "=r"(u[31])
+        : "r"(taddr)
+        : "memory");
+}
+// 128 columns: four loads in flight, one wait.  The empty statements tie the
+// registers to the wait, so that no use is scheduled before it.
+__device__ __forceinline__ void tmem_ld128(uint32_t taddr, float (&r)[128]) {
+#pragma unroll
+    for (int i = 0; i < 4; i++) tmem_ld32_async(taddr + 32 * i, r + 32 * i);
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 128; i++) asm volatile("" : "+f"(r[i]));
 }
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&r)[32]) {
     const uint32_t* u = reinterpret_cast<const uint32_t*>(r);

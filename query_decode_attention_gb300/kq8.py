@@ -101,6 +101,8 @@ _lib.kq8_tree_workspace_bytes.restype = _SZ
 _lib.kq8_tree_attn.argtypes = [_P, _P, _I32, _SZ, _SZ, _I32, _CP, _P, _I32, _P, _P, _P, _I32,
                                _I32, _I32, _I32, _I32, ctypes.c_float, _P, _SZ, _P]
 _lib.kq8_tree_commit.argtypes = [_CP, _I32, _P, _I32, _P, _P, _P, _I32, _I32, _P, _P]
+_lib.kq8_prompt_attn.argtypes = [_P, _P, _P, _P, _I32, _SZ, _SZ, _SZ, _SZ, _SZ, _SZ, _P, _I32,
+                                 _I32, _I32, _I32, _I32, ctypes.c_float, _P, _P]
 _lib.kq8_read_status.argtypes = [_P, ctypes.POINTER(ctypes.c_uint32), _P]
 _lib.kq8_strerror.argtypes = [ctypes.c_int]
 _lib.kq8_strerror.restype = ctypes.c_char_p
@@ -633,6 +635,30 @@ def kq8_tree_commit(cache: PagedKVCache, page_table: torch.Tensor, base_lens: to
     _check(_lib.kq8_tree_commit(ctypes.byref(cache.struct), cache.bits, _ptr(page_table),
                                 page_table.shape[1], _ptr(base_lens), _ptr(path), _ptr(path_len),
                                 path.shape[1], B, _ptr(status), st), "kq8_tree_commit")
+
+
+def kq8_prompt_attn(out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                    cu_seqlens: torch.Tensor, max_len: int, scale: float,
+                    status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Causal attention over packed prompts (include/kq8.h): q and out [total, nq,
+    128], k and v [total, nkv, 128] of float16 or bfloat16 (q, k, v of any token and
+    head stride), cu_seqlens int32 [B+1], no sequence longer than max_len."""
+    qp, kp, vp = _rows(q, "q"), _rows(k, "k"), _rows(v, "v")
+    for t, name in ((out, "out"), (k, "k"), (v, "v")):
+        _dtype(t, q.dtype, name)
+    _dtype(cu_seqlens, torch.int32, "cu_seqlens")
+    if out.shape != q.shape or k.shape != v.shape or k.shape[0] != q.shape[0]:
+        raise ValueError("q and out must be [total, nq, 128], k and v [total, nkv, 128]")
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must be [B+1]")
+    if status is not None:
+        _dtype(status, torch.int32, "status")
+    st = _stream_on(q.device, stream, out, k, v, cu_seqlens, status)
+    sq, sk, sv = q.stride(), k.stride(), v.stride()
+    _check(_lib.kq8_prompt_attn(_ptr(out), qp, kp, vp, DTYPES[q.dtype], sq[0], sq[1], sk[0], sk[1],
+                                sv[0], sv[1], _ptr(cu_seqlens), q.shape[0], int(max_len),
+                                cu_seqlens.numel() - 1, q.shape[1], k.shape[1], float(scale),
+                                _ptr(status), st), "kq8_prompt_attn")
 
 
 # ---- test-only exports -------------------------------------------------------
