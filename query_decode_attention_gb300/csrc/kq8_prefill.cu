@@ -277,8 +277,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) kq8_prefill_kernel(const Prefil
         };
         int32_t pw_cur = load_window(0), pw_nxt = load_window(1);
         int armed[PF_RAW] = {-1, -1, -1};  // last sub-tile whose copies went into each stage
-        uint64_t pol;
-        asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(pol));
+        const uint64_t pol = l2_evict_last_policy();
         for (int t = 0; t < 2 * nsteps; t++) {
             const int s = t % PF_RAW;
             if (t >= PF_RAW &&

@@ -156,8 +156,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
         if (warp == PR_LOAD_WARP && lane == 0) {
             // ---- loads: ring item 2 j is K of block j, 2 j + 1 its V
             const uint64_t pol = l2_evict_first_policy();
-            uint64_t keep;
-            asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(keep));
+            const uint64_t keep = l2_evict_last_policy();
             const uint32_t qbytes = (uint32_t)(TQ * G) * 128u;
             mbar_arrive_expect_tx(bars + PB_Q, 2 * qbytes * (nB ? 2 : 1));
             for (int t = 0; t < (nB ? 2 : 1); t++)
@@ -289,7 +288,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
             if (!ok) break;
             tc::fence_after_sync();
             float x[PR_BLK];
-            tc::tmem_ld128(tS, x);
+            tc::tmem_ld_cols<PR_BLK>(tS, x);
             if ((j + 1) * PR_BLK - 1 > first) {  // a diagonal block: token c sees 0 .. tok
                 const int vis = tok - j * PR_BLK;  // last visible column
 #pragma unroll

@@ -61,8 +61,8 @@ __device__ __forceinline__ uint64_t sdesc(uint32_t saddr, uint32_t lbo, uint32_t
 __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
     return sdesc(saddr, lbo, sbo) | (2ull << 61);
 }
-// Instruction descriptor bit 16: B is MN-major.
-constexpr uint32_t IDESC_B_MN = 1u << 16;
+// Instruction descriptor bits 15 and 16: A, B is MN-major.
+constexpr uint32_t IDESC_A_MN = 1u << 15, IDESC_B_MN = 1u << 16;
 
 // Instruction descriptor of kind::f16 with an fp32 accumulator, both operands
 // K-major: D format in bits 4-5 (1 = f32), A and B formats in bits 7-9 and
@@ -138,7 +138,7 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&r)[16]) {
         : "memory");
 }
 // 32 lanes x 32 columns without the wait: the registers hold the data after a
-// wait (tmem_ld128 below).
+// wait (tmem_ld_cols below).
 __device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, float* r) {
     uint32_t* u = reinterpret_cast<uint32_t*>(r);
     asm volatile(
@@ -154,14 +154,49 @@ __device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, float* r) {
         : "r"(taddr)
         : "memory");
 }
-// 128 columns: four loads in flight, one wait.  The empty statements tie the
-// registers to the wait, so that no use is scheduled before it.
-__device__ __forceinline__ void tmem_ld128(uint32_t taddr, float (&r)[128]) {
+__device__ __forceinline__ void tmem_ld16_async(uint32_t taddr, float* r) {
+    uint32_t* u = reinterpret_cast<uint32_t*>(r);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15}, [%16];"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]),
+          "=r"(u[7]), "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]),
+          "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
+        : "r"(taddr)
+        : "memory");
+}
+// N (16, or a multiple of 32) columns: all loads in flight, one wait.  The empty
+// statements tie the registers to the wait, so that no use is scheduled before it.
+template <int N>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, float (&r)[N]) {
+    if constexpr (N == 16) {
+        tmem_ld16_async(taddr, r);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; i++) tmem_ld32_async(taddr + 32 * i, r + 32 * i);
+        for (int i = 0; i < N / 32; i++) tmem_ld32_async(taddr + 32 * i, r + 32 * i);
+    }
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-    for (int i = 0; i < 128; i++) asm volatile("" : "+f"(r[i]));
+    for (int i = 0; i < N; i++) asm volatile("" : "+f"(r[i]));
+}
+// 8 columns, load and store with their waits.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&r)[8]) {
+    uint32_t* u = reinterpret_cast<uint32_t*>(r);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]),
+          "=r"(u[7])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const float (&r)[8]) {
+    const uint32_t* u = reinterpret_cast<const uint32_t*>(r);
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n\t"
+        "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+        "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+        : "memory");
 }
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&r)[32]) {
     const uint32_t* u = reinterpret_cast<const uint32_t*>(r);

@@ -31,26 +31,17 @@
 // modulo 8, so the 128-byte swizzle keeps that load free of conflicts too.
 // The weights therefore go from accumulators to operands within the lane.
 #include <cuda_bf16.h>
-#include <cuda_fp16.h>
 
 #include <cstring>
 #include <type_traits>
 
-#include "kq8_internal.h"
 #include "kq8_common.cuh"
+#include "kq8_internal.h"
 
 namespace kq8 {
 namespace {
 
-constexpr int TR_WARPS = 4;
-constexpr int TR_THREADS = TR_WARPS * 32;
-constexpr int TR_STAGES = 2;
-constexpr int TR_ROWS = 16;
-constexpr int TR_MAX_CHUNK = 128;       // sub-tiles per chunk, see tree_plan
 constexpr float TR_LOG2E = 1.4426950408889634f;
-// Lazy rescale: between rescales a weight stays below 2^TR_SLACK.
-constexpr float TR_SLACK = 8.0f;
-
 constexpr size_t TR_STATUS_BYTES = 256;
 constexpr size_t TR_COUNTERS = 16384;
 constexpr size_t TR_HEADER = TR_STATUS_BYTES + TR_COUNTERS * sizeof(uint32_t);
@@ -74,22 +65,10 @@ struct TreeParams {
     int32_t nq, G;
     float scale;
     int32_t chunk_tiles, num_chunks, row_tiles;
-    float* part_acc;       // [pairs][16][num_chunks][HD]
-    float2* part_ms;       // [pairs][16][num_chunks]
+    float* part_acc;       // [pairs][tile's rows][num_chunks][HD]
+    float2* part_ms;       // [pairs][tile's rows][num_chunks]
     uint32_t* status;
     uint32_t* counters;    // [pairs]
-};
-
-struct TreeSmem {
-    alignas(1024) uint8_t v[TR_WARPS][TR_STAGES][SUB_V_BYTES];
-    alignas(128) uint8_t k[TR_WARPS][TR_STAGES][SUB_K_BYTES];
-    alignas(16) float sc[TR_WARPS][TR_STAGES][2][TILE];  // kscale, vscale as stored
-    alignas(16) float mul[TR_WARPS][2][TILE];            // score multiplier, weight multiplier
-    alignas(16) int8_t qi[TR_ROWS][HD];
-    alignas(16) float qsc[TR_ROWS][NB];
-    alignas(16) float2 ms[TR_WARPS][TR_ROWS];
-    alignas(8) uint64_t bar[TR_WARPS][TR_STAGES];
-    int last;
 };
 
 __device__ __forceinline__ float tr_ex2(float x) {
@@ -143,11 +122,41 @@ __device__ __forceinline__ uint32_t node_window(const TreeParams& P, int64_t row
     return __funnelshift_r(word(w), s ? word(w + 1) : 0u, s);
 }
 
-template <bool HILO>
-__global__ void __launch_bounds__(TR_THREADS, 3)
+constexpr int TR_WARPS = 4;
+constexpr int TR_THREADS = TR_WARPS * 32;
+constexpr int TR_MAX_CHUNK = 128;       // sub-tiles per chunk, see tree_plan
+// Lazy rescale: between rescales a weight stays below 2^TR_SLACK.
+constexpr float TR_SLACK = 8.0f;
+
+// MT: tiles of 16 rows that a warp holds.  One where the rows fit it: 3 CTAs per SM
+// at 168 registers; else two: every widened K and V code serves 32 rows, 2 CTAs per
+// SM with a third ring stage.
+template <int MT>
+struct TreeShape {
+    static constexpr int ROWS = 16 * MT, STAGES = MT == 1 ? 2 : 3, CTAS = MT == 1 ? 3 : 2;
+};
+template <int MT>
+struct TreeSmem {
+    static constexpr int ROWS = TreeShape<MT>::ROWS, STAGES = TreeShape<MT>::STAGES;
+    // the two rings, and after the walk the warps' accumulators [warp][ROWS][HD]
+    alignas(1024) uint8_t v[TR_WARPS][STAGES][SUB_V_BYTES];
+    alignas(128) uint8_t k[TR_WARPS][STAGES][SUB_K_BYTES];
+    alignas(16) float sc[TR_WARPS][STAGES][2][TILE];  // kscale, vscale as stored
+    alignas(16) float mul[TR_WARPS][2][TILE];         // score multiplier, V step
+    // Q's codes as fp16 A fragments: [16-row tile][element block][k-step][lane]
+    alignas(16) uint4 qf[MT][NB][2][32];
+    alignas(16) float qsc[ROWS][NB];
+    alignas(16) float2 ms[TR_WARPS][ROWS];
+    alignas(8) uint64_t bar[TR_WARPS][STAGES];
+    int last;
+};
+
+template <int MT, bool HILO>
+__global__ void __launch_bounds__(TR_THREADS, TreeShape<MT>::CTAS)
     kq8_tree_kernel(const __grid_constant__ TreeParams P) {
+    constexpr int TR_ROWS = TreeShape<MT>::ROWS, TR_STAGES = TreeShape<MT>::STAGES;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    TreeSmem& S = *reinterpret_cast<TreeSmem*>(
+    TreeSmem<MT>& S = *reinterpret_cast<TreeSmem<MT>*>(
         smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int gq = lane >> 2, c4 = lane & 3;
@@ -231,193 +240,227 @@ __global__ void __launch_bounds__(TR_THREADS, 3)
             x = load_q4(P.q, P.dtype, (int64_t)(q0 + node) * P.q_st + hq * P.q_sh + 4 * lane);
         }
         float qs;
-        const uint32_t codes = quantize_q_lane(x, qs);
-        reinterpret_cast<uint32_t*>(S.qi[r])[lane] = codes;
+        const uint32_t u = quantize_q_lane(x, qs) ^ 0x80808080u;
+        // this lane's codes are elements 8c + 4s .. + 3 of block lane / 8, c = lane % 8 / 2,
+        // s = lane % 2: registers half and half + 2 of k-step s for lane (row % 8, c)
+        uint32_t* f = reinterpret_cast<uint32_t*>(
+            &S.qf[r >> 4][lane >> 3][lane & 1][(r & 7) * 4 + ((lane & 7) >> 1)]);
+        f[(r >> 3) & 1] = hsub2(__byte_perm(u, 0x64646464u, 0x4140), 0x64806480u);
+        f[((r >> 3) & 1) + 2] = hsub2(__byte_perm(u, 0x64646464u, 0x4342), 0x64806480u);
         if ((lane & 7) == 0) S.qsc[r][lane >> 3] = qs;
     }
     __syncthreads();
-    // A operand of the scores: k-step s of block bb takes elements 8c + 4s ..
-    // + 3 of the block (K's pieces are read in the same order)
-    uint32_t qa[NB][2][4];
-    float qsc[2][NB];
-#pragma unroll
-    for (int half = 0; half < 2; half++)
-#pragma unroll
-        for (int bb = 0; bb < NB; bb++) {
-            qsc[half][bb] = S.qsc[gq + 8 * half][bb];
-            const uint2 w = *reinterpret_cast<const uint2*>(&S.qi[gq + 8 * half][bb * 32 + 8 * c4]);
-            const uint32_t u[2] = {w.x ^ 0x80808080u, w.y ^ 0x80808080u};
-#pragma unroll
-            for (int s = 0; s < 2; s++) {
-                qa[bb][s][half] = hsub2(__byte_perm(u[s], 0x64646464u, 0x4140), 0x64806480u);
-                qa[bb][s][half + 2] = hsub2(__byte_perm(u[s], 0x64646464u, 0x4342), 0x64806480u);
-            }
-        }
 
-    // rows gq and gq + 8: running max (base 2), partial sum over this lane's
-    // tokens; O: D[cg][0] elements 16cg + 2j, D[cg][1] 16cg + 2j + 1 (column j)
-    float M[2] = {M_INIT, M_INIT}, sum[2] = {0.0f, 0.0f};
-    float D[HD / 16][2][4];
+    // Row half of 16-row tile mt is 16 mt + gq + 8 half.  Per row: running max (base
+    // 2), partial sum over this lane's tokens, and O: D[mt][cg][0] elements 16cg + 2j,
+    // D[mt][cg][1] 16cg + 2j + 1 (column j)
+    float M[MT][2], sum[MT][2];
+    float D[MT][HD / 16][2][4];
+    // a row's weights go to the matrix instructions scaled by 2^-ev; per row, so that
+    // what a row does not see cannot cost it precision
+    int ev[MT][2];
 #pragma unroll
-    for (int cg = 0; cg < HD / 16; cg++)
+    for (int mt = 0; mt < MT; mt++) {
 #pragma unroll
-        for (int j = 0; j < 4; j++) D[cg][0][j] = D[cg][1][j] = 0.0f;
-    // the weights of row half go to the matrix instructions scaled by 2^-ev[half];
-    // per row, so that what a row does not see cannot cost it precision
-    int ev[2] = {-126, -126};
+        for (int half = 0; half < 2; half++) {
+            M[mt][half] = M_INIT;
+            sum[mt][half] = 0.0f;
+            ev[mt][half] = -126;
+        }
+#pragma unroll
+        for (int cg = 0; cg < HD / 16; cg++)
+#pragma unroll
+            for (int j = 0; j < 4; j++) D[mt][cg][0][j] = D[mt][cg][1][j] = 0.0f;
+    }
     const float kmul = inv127() * P.scale * TR_LOG2E;
+    auto scale_row = [&](int mt, int half, float f) {
+#pragma unroll
+        for (int cg = 0; cg < HD / 16; cg++)
+#pragma unroll
+            for (int j = 0; j < 2; j++) {
+                D[mt][cg][j][2 * half] *= f;
+                D[mt][cg][j][2 * half + 1] *= f;
+            }
+    };
 
     auto step = [&](int st, int tile, auto masked_c) {
         constexpr bool MASKED = decltype(masked_c)::value;
-        const uint8_t* kst = S.k[warp][st];
-        uint32_t win[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};  // visible tokens of the two rows
-        if (MASKED) {
-#pragma unroll
-            for (int half = 0; half < 2; half++) {
-                const int r = gq + 8 * half;
-                win[half] = r < rows ? node_window(P, q0, (rt * TR_ROWS + r) / G, nb,
-                                                   tile * TILE - base)
-                                     : 0u;
-            }
-        }
         // lane = token: its score multiplier and V step.  A token past the end gets
         // 0 for both: what its row of the page holds must not matter.
         const bool live = !MASKED || tile * TILE + lane < n;
         const float vstep = live ? __fmul_rn(S.sc[warp][st][1][lane], inv127()) : 0.0f;
         S.mul[warp][0][lane] = live ? __fmul_rn(S.sc[warp][st][0][lane], kmul) : 0.0f;
         S.mul[warp][1][lane] = vstep;
+        auto bits = [](float x) -> uint32_t {  // of a finite |x|, else 0
+            const uint32_t u = __float_as_uint(x) & 0x7FFFFFFFu;
+            return u < 0x7F800000u ? u : 0u;
+        };
+        const uint32_t vtop = MASKED ? 0u : __reduce_max_sync(0xffffffffu, bits(vstep));
         __syncwarp();
-        float2 km[4], vm[4];
+        // ---- scores: s[mt][i][half] = (token 8c + r_i, token 8c + 4 + r_i), r_i = (i + c) % 4
+        float2 s[MT][4][2];
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const int t = 8 * c4 + ((i + c4) & 3);
-            km[i] = make_float2(S.mul[warp][0][t], S.mul[warp][0][t + 4]);
-            vm[i] = make_float2(S.mul[warp][1][t], S.mul[warp][1][t + 4]);
-        }
-        // ev keeps the largest V step that the row sees times 2^-ev below 2^7, so with
-        // p <= 2^8 a weight stays below 2^15, inside the fp16 range; a tile that needs
-        // a larger ev first scales the row of O by the exact power of two 2^(old - new).
-        // A step that is not finite does not count: its row is lost where it is seen.
-        {
-            auto bits = [](float x) -> uint32_t {
-                const uint32_t u = __float_as_uint(x) & 0x7FFFFFFFu;
-                return u < 0x7F800000u ? u : 0u;
-            };
-            uint32_t vb[2];
-            if (!MASKED) {
-                vb[0] = vb[1] = __reduce_max_sync(0xffffffffu, bits(vstep));
-            } else {
+        for (int bb = 0; bb < NB; bb++) {
+            uint2 w[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                w[i] = *reinterpret_cast<const uint2*>(
+                    S.k[warp][st] + 1024 * bb + (8 * ((i + (gq >> 1)) & 3) + gq) * 32 + 8 * c4);
+            float d[MT][4][4];
+#pragma unroll
+            for (int ks = 0; ks < 2; ks++) {
+                uint32_t qa[MT][4];
+#pragma unroll
+                for (int mt = 0; mt < MT; mt++) {
+                    const uint4 f = S.qf[mt][bb][ks][lane];
+                    qa[mt][0] = f.x;
+                    qa[mt][1] = f.y;
+                    qa[mt][2] = f.z;
+                    qa[mt][3] = f.w;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const uint32_t u = (ks ? w[i].y : w[i].x) ^ 0x80808080u;
+                    const uint32_t b0 = hsub2(__byte_perm(u, 0x64646464u, 0x4140), 0x64806480u);
+                    const uint32_t b1 = hsub2(__byte_perm(u, 0x64646464u, 0x4342), 0x64806480u);
+#pragma unroll
+                    for (int mt = 0; mt < MT; mt++) {
+                        if (ks == 0) d[mt][i][0] = d[mt][i][1] = d[mt][i][2] = d[mt][i][3] = 0.0f;
+                        mma_f16_16816(d[mt][i], qa[mt], b0, b1);
+                    }
+                }
+            }
+#pragma unroll
+            for (int mt = 0; mt < MT; mt++)
 #pragma unroll
                 for (int half = 0; half < 2; half++) {
-                    vb[half] = 0u;
+                    const float qs = S.qsc[16 * mt + gq + 8 * half][bb];
+                    const float2 q2 = make_float2(qs, qs);
 #pragma unroll
                     for (int i = 0; i < 4; i++) {
-                        const int t = 8 * c4 + ((i + c4) & 3);
-                        if ((win[half] >> t) & 1u) vb[half] = max(vb[half], bits(vm[i].x));
-                        if ((win[half] >> (t + 4)) & 1u) vb[half] = max(vb[half], bits(vm[i].y));
+                        const float2 dv = make_float2(d[mt][i][2 * half], d[mt][i][2 * half + 1]);
+                        s[mt][i][half] = bb == 0 ? __fmul2_rn(dv, q2) : __ffma2_rn(dv, q2, s[mt][i][half]);
                     }
-                    vb[half] = max(vb[half], __shfl_xor_sync(0xffffffffu, vb[half], 1));
-                    vb[half] = max(vb[half], __shfl_xor_sync(0xffffffffu, vb[half], 2));
                 }
-            }
-            const int en[2] = {max(ev[0], (int)(vb[0] >> 23) - 133), max(ev[1], (int)(vb[1] >> 23) - 133)};
-            if (__any_sync(0xffffffffu, en[0] != ev[0] || en[1] != ev[1])) {  // rare
-#pragma unroll
-                for (int half = 0; half < 2; half++) {
-                    const float f = (ev[half] - en[half] >= -126) ? pow2i(ev[half] - en[half]) : 0.0f;
-#pragma unroll
-                    for (int cg = 0; cg < HD / 16; cg++)
-#pragma unroll
-                        for (int j = 0; j < 2; j++) {
-                            D[cg][j][2 * half] *= f;
-                            D[cg][j][2 * half + 1] *= f;
-                        }
-                    ev[half] = en[half];
-                }
-            }
         }
-        const float vsc[2] = {pow2i(-ev[0]), pow2i(-ev[1])};
-        // ---- scores: s[i][half] = (token 8c + r_i, token 8c + 4 + r_i), r_i = (i + c) % 4
-        float2 s[4][2];
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const uint8_t* kp = kst + (8 * ((i + (gq >> 1)) & 3) + gq) * 32 + 8 * c4;
-#pragma unroll
-            for (int bb = 0; bb < NB; bb++) {
-                const uint2 w = *reinterpret_cast<const uint2*>(kp + 1024 * bb);
-                const uint32_t u0 = w.x ^ 0x80808080u, u1 = w.y ^ 0x80808080u;
-                float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                mma_f16_16816(d, qa[bb][0],
-                              hsub2(__byte_perm(u0, 0x64646464u, 0x4140), 0x64806480u),
-                              hsub2(__byte_perm(u0, 0x64646464u, 0x4342), 0x64806480u));
-                mma_f16_16816(d, qa[bb][1],
-                              hsub2(__byte_perm(u1, 0x64646464u, 0x4140), 0x64806480u),
-                              hsub2(__byte_perm(u1, 0x64646464u, 0x4342), 0x64806480u));
-#pragma unroll
-                for (int half = 0; half < 2; half++) {
-                    const float2 dv = make_float2(d[2 * half], d[2 * half + 1]);
-                    const float2 q2 = make_float2(qsc[half][bb], qsc[half][bb]);
-                    s[i][half] = bb == 0 ? __fmul2_rn(dv, q2) : __ffma2_rn(dv, q2, s[i][half]);
-                }
-            }
-        }
+        uint32_t win[MT][2];  // visible tokens of the rows
         bool grow = false;
-        bool on[4][2][2];
+        {
+            float2 km[4];
 #pragma unroll
-        for (int i = 0; i < 4; i++)
-#pragma unroll
-            for (int half = 0; half < 2; half++) {
-                s[i][half] = __fmul2_rn(s[i][half], km[i]);
-                if (MASKED) {
-                    const int t = 8 * c4 + ((i + c4) & 3);
-                    on[i][half][0] = (win[half] >> t) & 1u;
-                    on[i][half][1] = (win[half] >> (t + 4)) & 1u;
-                    s[i][half].x = on[i][half][0] ? s[i][half].x : -INFINITY;
-                    s[i][half].y = on[i][half][1] ? s[i][half].y : -INFINITY;
-                }
-                grow |= fmaxf(s[i][half].x, s[i][half].y) > M[half] + TR_SLACK;
+            for (int i = 0; i < 4; i++) {
+                const int t = 8 * c4 + ((i + c4) & 3);
+                km[i] = make_float2(S.mul[warp][0][t], S.mul[warp][0][t + 4]);
             }
+#pragma unroll
+            for (int mt = 0; mt < MT; mt++)
+#pragma unroll
+                for (int half = 0; half < 2; half++) {
+                    if (MASKED) {
+                        const int r = 16 * mt + gq + 8 * half;
+                        win[mt][half] = r < rows ? node_window(P, q0, (rt * TR_ROWS + r) / G, nb,
+                                                               tile * TILE - base)
+                                                 : 0u;
+                    }
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        float2& x = s[mt][i][half];
+                        x = __fmul2_rn(x, km[i]);
+                        if (MASKED) {
+                            const int t = 8 * c4 + ((i + c4) & 3);
+                            x.x = (win[mt][half] >> t) & 1u ? x.x : -INFINITY;
+                            x.y = (win[mt][half] >> (t + 4)) & 1u ? x.y : -INFINITY;
+                        }
+                        top = fmaxf(top, fmaxf(x.x, x.y));
+                    }
+                    grow |= top > M[mt][half] + TR_SLACK;
+                }
+        }
         if (__any_sync(0xffffffffu, grow)) {
             // rare: some row's maximum grew by a wide margin -> rescale its state
 #pragma unroll
-            for (int half = 0; half < 2; half++) {
-                float m = M[half];
+            for (int mt = 0; mt < MT; mt++)
 #pragma unroll
-                for (int i = 0; i < 4; i++) m = fmaxf(m, fmaxf(s[i][half].x, s[i][half].y));
-                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-                const float f = tr_ex2(M[half] - m);
-                M[half] = m;
-                sum[half] *= f;
+                for (int half = 0; half < 2; half++) {
+                    float m = M[mt][half];
 #pragma unroll
-                for (int cg = 0; cg < HD / 16; cg++)
-#pragma unroll
-                    for (int j = 0; j < 2; j++) {
-                        D[cg][j][2 * half] *= f;
-                        D[cg][j][2 * half + 1] *= f;
-                    }
-            }
-        }
-        // ---- weights: token pair i of row half -> A register (half + 2 (i % 2)) of
-        // k-step i / 2
-        uint32_t hi[2][4], lo[2][4];
-#pragma unroll
-        for (int i = 0; i < 4; i++)
-#pragma unroll
-            for (int half = 0; half < 2; half++) {
-                const float2 y = __fadd2_rn(s[i][half], make_float2(-M[half], -M[half]));
-                const float2 p = make_float2(tr_ex2(y.x), tr_ex2(y.y));
-                sum[half] += p.x + p.y;
-                float2 w = __fmul2_rn(p, __fmul2_rn(vm[i], make_float2(vsc[half], vsc[half])));
-                if (MASKED) {  // a masked token's V step may be anything
-                    w.x = on[i][half][0] ? w.x : 0.0f;
-                    w.y = on[i][half][1] ? w.y : 0.0f;
+                    for (int i = 0; i < 4; i++)
+                        m = fmaxf(m, fmaxf(s[mt][i][half].x, s[mt][i][half].y));
+                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+                    const float f = tr_ex2(M[mt][half] - m);
+                    M[mt][half] = m;
+                    sum[mt][half] *= f;
+                    scale_row(mt, half, f);
                 }
-                const uint32_t wh = f2_to_h2(w.x, w.y);
-                hi[i >> 1][half + 2 * (i & 1)] = wh;
-                if (HILO) {
-                    const float2 back = h2_to_f2(wh);
-                    lo[i >> 1][half + 2 * (i & 1)] = f2_to_h2(w.x - back.x, w.y - back.y);
+        }
+        // ---- weights.  ev keeps the largest V step that the row sees times 2^-ev below
+        // 2^7, so with p <= 2^8 a weight stays below 2^15, inside the fp16 range; a tile
+        // that needs a larger ev first scales the row of O by the exact power of two
+        // 2^(old - new).  A step that is not finite does not count: its row is lost where
+        // it is seen.
+        float2 vm[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const int t = 8 * c4 + ((i + c4) & 3);
+            vm[i] = make_float2(S.mul[warp][1][t], S.mul[warp][1][t + 4]);
+        }
+        bool wide = false;
+        int en[MT][2];
+#pragma unroll
+        for (int mt = 0; mt < MT; mt++)
+#pragma unroll
+            for (int half = 0; half < 2; half++) {
+                uint32_t vb = vtop;
+                if (MASKED) {
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        const int t = 8 * c4 + ((i + c4) & 3);
+                        if ((win[mt][half] >> t) & 1u) vb = max(vb, bits(vm[i].x));
+                        if ((win[mt][half] >> (t + 4)) & 1u) vb = max(vb, bits(vm[i].y));
+                    }
+                    vb = max(vb, __shfl_xor_sync(0xffffffffu, vb, 1));
+                    vb = max(vb, __shfl_xor_sync(0xffffffffu, vb, 2));
+                }
+                en[mt][half] = max(ev[mt][half], (int)(vb >> 23) - 133);
+                wide |= en[mt][half] != ev[mt][half];
+            }
+        if (__any_sync(0xffffffffu, wide)) {
+#pragma unroll
+            for (int mt = 0; mt < MT; mt++)
+#pragma unroll
+                for (int half = 0; half < 2; half++) {
+                    const int by = ev[mt][half] - en[mt][half];
+                    scale_row(mt, half, by >= -126 ? pow2i(by) : 0.0f);
+                    ev[mt][half] = en[mt][half];
+                }
+        }
+        // token pair i of row half -> A register (half + 2 (i % 2)) of k-step i / 2
+        uint32_t hi[MT][2][4], lo[MT][2][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; mt++)
+#pragma unroll
+            for (int half = 0; half < 2; half++) {
+                const float vsc = pow2i(-ev[mt][half]);
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const float2 y = __fadd2_rn(s[mt][i][half],
+                                                make_float2(-M[mt][half], -M[mt][half]));
+                    const float2 p = make_float2(tr_ex2(y.x), tr_ex2(y.y));
+                    sum[mt][half] += p.x + p.y;
+                    float2 w = __fmul2_rn(p, __fmul2_rn(vm[i], make_float2(vsc, vsc)));
+                    if (MASKED) {  // a masked token's V step may be anything
+                        const int t = 8 * c4 + ((i + c4) & 3);
+                        w.x = (win[mt][half] >> t) & 1u ? w.x : 0.0f;
+                        w.y = (win[mt][half] >> (t + 4)) & 1u ? w.y : 0.0f;
+                    }
+                    const uint32_t wh = f2_to_h2(w.x, w.y);
+                    hi[mt][i >> 1][half + 2 * (i & 1)] = wh;
+                    if (HILO) {
+                        const float2 back = h2_to_f2(wh);
+                        lo[mt][i >> 1][half + 2 * (i & 1)] = f2_to_h2(w.x - back.x, w.y - back.y);
+                    }
                 }
             }
         // ---- values: lane L gives the V row tok(L / 8, L % 8) of each 16-byte chunk
@@ -435,14 +478,16 @@ __global__ void __launch_bounds__(TR_THREADS, 3)
                 bo[j] = hsub2(__byte_perm(u, 0x64646464u, 0x4341), 0x64806480u);
             }
 #pragma unroll
-            for (int ks = 0; ks < 2; ks++) {
-                mma_f16_16816(D[cg][0], hi[ks], be[2 * ks], be[2 * ks + 1]);
-                mma_f16_16816(D[cg][1], hi[ks], bo[2 * ks], bo[2 * ks + 1]);
-                if (HILO) {
-                    mma_f16_16816(D[cg][0], lo[ks], be[2 * ks], be[2 * ks + 1]);
-                    mma_f16_16816(D[cg][1], lo[ks], bo[2 * ks], bo[2 * ks + 1]);
+            for (int ks = 0; ks < 2; ks++)
+#pragma unroll
+                for (int mt = 0; mt < MT; mt++) {
+                    mma_f16_16816(D[mt][cg][0], hi[mt][ks], be[2 * ks], be[2 * ks + 1]);
+                    mma_f16_16816(D[mt][cg][1], hi[mt][ks], bo[2 * ks], bo[2 * ks + 1]);
+                    if (HILO) {
+                        mma_f16_16816(D[mt][cg][0], lo[mt][ks], be[2 * ks], be[2 * ks + 1]);
+                        mma_f16_16816(D[mt][cg][1], lo[mt][ks], bo[2 * ks], bo[2 * ks + 1]);
+                    }
                 }
-            }
         }
     };
 
@@ -474,22 +519,26 @@ __global__ void __launch_bounds__(TR_THREADS, 3)
         if (i + TR_STAGES < mine) issue(i + TR_STAGES);
     }
 
-    // ---- merge the warps (the V ring becomes [warp][16][HD] accumulators)
+    // ---- merge the warps (the rings become [warp][rows][HD] accumulators)
     const bool cta_failed = __syncthreads_or(failed ? 1 : 0) != 0;
     float* macc = reinterpret_cast<float*>(S.v);
 #pragma unroll
-    for (int half = 0; half < 2; half++) {
-        sum[half] += __shfl_xor_sync(0xffffffffu, sum[half], 1);
-        sum[half] += __shfl_xor_sync(0xffffffffu, sum[half], 2);
-        const float f = pow2i(ev[half]);
-        float* row = macc + (warp * TR_ROWS + gq + 8 * half) * HD;
+    for (int mt = 0; mt < MT; mt++)
 #pragma unroll
-        for (int cg = 0; cg < HD / 16; cg++)
-            *reinterpret_cast<float4*>(row + 16 * cg + 4 * c4) =
-                make_float4(D[cg][0][2 * half] * f, D[cg][1][2 * half] * f,
-                            D[cg][0][2 * half + 1] * f, D[cg][1][2 * half + 1] * f);
-        if (c4 == 0) S.ms[warp][gq + 8 * half] = make_float2(M[half], sum[half]);
-    }
+        for (int half = 0; half < 2; half++) {
+            float t = sum[mt][half];
+            t += __shfl_xor_sync(0xffffffffu, t, 1);
+            t += __shfl_xor_sync(0xffffffffu, t, 2);
+            const float f = pow2i(ev[mt][half]);
+            const int r = 16 * mt + gq + 8 * half;
+            float* row = macc + (warp * TR_ROWS + r) * HD;
+#pragma unroll
+            for (int cg = 0; cg < HD / 16; cg++)
+                *reinterpret_cast<float4*>(row + 16 * cg + 4 * c4) =
+                    make_float4(D[mt][cg][0][2 * half] * f, D[mt][cg][1][2 * half] * f,
+                                D[mt][cg][0][2 * half + 1] * f, D[mt][cg][1][2 * half + 1] * f);
+            if (c4 == 0) S.ms[warp][r] = make_float2(M[mt][half], t);
+        }
     __syncthreads();
     const size_t pair = ((size_t)blockIdx.z * nkv + h) * P.row_tiles + rt;
     auto out_at = [&](int r) -> size_t {
@@ -563,16 +612,43 @@ __global__ void __launch_bounds__(TR_THREADS, 3)
     if (threadIdx.x == 0) P.counters[pair] = 0;  // ready for the next call
 }
 
-// A call's split: sequences per launch (so that the tickets of a launch fit the
-// header's counters), row tiles, chunks and the partials' places.
+// A call's split: rows of a tile, sequences per launch (so that the tickets of a
+// launch fit the header's counters), row tiles, chunks and the partials' places.
 struct TreePlan {
+    int tile_rows = 16;
     int seqs = 0, row_tiles = 1, chunk_tiles = TR_WARPS, num_chunks = 1;
     size_t off_ms = 0, off_acc = 0, total = TR_HEADER;
 };
+constexpr int64_t TR_PARTS = 512ll << 20;  // bytes of partials a call may take
+
+// Sub-tiles per chunk, at most TR_MAX_CHUNK (a long chunk of a ragged batch is a long
+// tail): of the chunk counts that allow, the one whose waves of resident CTAs take
+// least, a CTA's prologue and merge costing TR_CTA_TILES sub-tiles of a warp beside its
+// walk.  Uniform lists of 512 sub-tiles, 128 of them, 32 rows: chunks of 56 in 4.2
+// waves 192 us, of 76 in 2.9 waves 160 us.
+constexpr int64_t TR_CTA_TILES = 5;
+int64_t tree_chunk(int64_t pairs, int64_t tiles, int ctas_per_sm) {
+    const int64_t slots = (int64_t)device_sms() * ctas_per_sm;
+    const int64_t least = (tiles + TR_MAX_CHUNK - 1) / TR_MAX_CHUNK;
+    int64_t best = TR_WARPS, cost = INT64_MAX;
+    for (int64_t k = least > 1 ? least : 1; k <= 4 * least + 16; k++) {
+        const int64_t c = ((tiles + k - 1) / k + TR_WARPS - 1) / TR_WARPS * TR_WARPS;
+        if (c < TR_WARPS) break;
+        const int64_t waves = (pairs * ((tiles + c - 1) / c) + slots - 1) / slots;
+        if (waves * (c / TR_WARPS + TR_CTA_TILES) < cost) {
+            cost = waves * (c / TR_WARPS + TR_CTA_TILES);
+            best = c;
+        }
+        if (c == TR_WARPS) break;
+    }
+    return best;
+}
+
 TreePlan tree_plan(int B, int nq, int nkv, int max_seq_len, int max_q_len) {
     TreePlan p;
     const int64_t rows = (int64_t)max_q_len * (nq / nkv);
-    p.row_tiles = (int)((rows + TR_ROWS - 1) / TR_ROWS);
+    p.tile_rows = rows <= 16 ? 16 : 32;
+    p.row_tiles = (int)((rows + p.tile_rows - 1) / p.tile_rows);
     if (p.row_tiles < 1) p.row_tiles = 1;
     const int64_t per_seq = (int64_t)nkv * p.row_tiles;
     if (per_seq > (int64_t)TR_COUNTERS) return p;  // seqs = 0: unsupported
@@ -580,50 +656,37 @@ TreePlan tree_plan(int B, int nq, int nkv, int max_seq_len, int max_q_len) {
     if (p.seqs > B) p.seqs = B;
     const int64_t pairs = (int64_t)p.seqs * per_seq;
     const int64_t tiles = ((int64_t)max_seq_len + TILE - 1) / TILE;
-    // As the exact decode splits its lists: one wave of resident CTAs (3 per SM)
-    // where every list fits it with chunks of at most TR_MAX_CHUNK sub-tiles, at
-    // most 16 chunks a list; else about four waves, with long chunks, because a
-    // CTA streams nothing in its prologue and merge.  Chunks grow past
-    // TR_MAX_CHUNK only to keep the partials under 512 MB.
-    const int64_t slots = (int64_t)device_sms() * 3;
-    int64_t per = pairs > 0 ? slots / pairs : slots;
-    if (per > 16) per = 16;
-    int64_t c = per >= 1 && (tiles + per - 1) / per <= TR_MAX_CHUNK
-                    ? (tiles + per - 1) / per
-                    : (pairs * tiles + 4 * slots - 1) / (4 * slots);
-    if (c > TR_MAX_CHUNK) c = TR_MAX_CHUNK;
-    c = (c + TR_WARPS - 1) / TR_WARPS * TR_WARPS;
-    if (c < TR_WARPS) c = TR_WARPS;
-    constexpr int64_t PART = (int64_t)TR_ROWS * (HD * sizeof(float) + sizeof(float2));
-    while (c < tiles && pairs * ((tiles + c - 1) / c) * PART > (512ll << 20)) c *= 2;
+    int64_t c = tree_chunk(pairs, tiles, p.tile_rows == 16 ? TreeShape<1>::CTAS : TreeShape<2>::CTAS);
+    const int64_t part = (int64_t)p.tile_rows * (HD * sizeof(float) + sizeof(float2));
+    while (c < tiles && pairs * ((tiles + c - 1) / c) * part > TR_PARTS) c *= 2;
     p.chunk_tiles = (int)c;
     p.num_chunks = tiles > 0 ? (int)((tiles + c - 1) / c) : 1;
+    const size_t parts = p.num_chunks > 1 ? (size_t)(pairs * p.tile_rows * p.num_chunks) : 0;
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-    const size_t parts = (size_t)pairs * TR_ROWS * p.num_chunks;
     p.off_ms = TR_HEADER;
     p.off_acc = up(p.off_ms + parts * sizeof(float2));
     p.total = up(p.off_acc + parts * HD * sizeof(float));
     return p;
 }
 
-constexpr size_t TR_SMEM = sizeof(TreeSmem) + 1024;  // slack to round the base up
-
-template <bool HILO>
+template <int MT, bool HILO>
 int launch_tree(const TreeParams& p, dim3 grid, cudaStream_t s) {
-    if (cudaFuncSetAttribute(kq8_tree_kernel<HILO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)TR_SMEM) != cudaSuccess)
+    constexpr size_t smem = sizeof(TreeSmem<MT>) + 1024;  // slack to round the base up
+    if (cudaFuncSetAttribute(kq8_tree_kernel<MT, HILO>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)smem) != cudaSuccess)
         return KQ8_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(TR_THREADS);
-    cfg.dynamicSmemBytes = TR_SMEM;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kq8_tree_kernel<HILO>, p) != cudaSuccess) return KQ8_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, kq8_tree_kernel<MT, HILO>, p) != cudaSuccess) return KQ8_ERR_CUDA;
     return cudaPeekAtLastError() == cudaSuccess ? KQ8_OK : KQ8_ERR_CUDA;
 }
 
@@ -701,11 +764,15 @@ int kq8_tree_attn(void* out, const void* q, int32_t dtype, size_t q_token_stride
     p.part_acc = reinterpret_cast<float*>(ws + plan.off_acc);
     p.status = reinterpret_cast<uint32_t*>(ws);
     p.counters = reinterpret_cast<uint32_t*>(ws + TR_STATUS_BYTES);
+    const cudaStream_t st = (cudaStream_t)stream;
+    const bool hilo = dtype != KQ8_BF16;
     for (p.b0 = 0; p.b0 < B; p.b0 += plan.seqs) {
         const int seqs = B - p.b0 < plan.seqs ? B - p.b0 : plan.seqs;
         const dim3 grid((unsigned)(plan.num_chunks * plan.row_tiles), (unsigned)nkv, (unsigned)seqs);
-        rc = dtype == KQ8_BF16 ? launch_tree<false>(p, grid, (cudaStream_t)stream)
-                               : launch_tree<true>(p, grid, (cudaStream_t)stream);
+        if (plan.tile_rows == 16)
+            rc = hilo ? launch_tree<1, true>(p, grid, st) : launch_tree<1, false>(p, grid, st);
+        else
+            rc = hilo ? launch_tree<2, true>(p, grid, st) : launch_tree<2, false>(p, grid, st);
         if (rc) return rc;
     }
     return KQ8_OK;

@@ -160,6 +160,9 @@ class Case:
     (5, 1, [333], [33], 256),                            # G = 5
     (4, 4, [31, 32, 33, 63, 64, 65], [1, 2, 31, 32, 33, 65], 32),  # sub-tile borders, G = 1
     (7, 1, [130], [1], 32),                              # G = 7, one node
+    (4, 1, [900, 5000], [12, 4], 32),                    # 48 rows; a sequence in several chunks
+    (8, 2, [3000, 129, 127], [8, 8, 5], 64),             # 32 rows, several chunks
+    (24, 3, [4097, 300], [16, 2], 32),                   # 128 rows, G = 8
 ])
 def test_tree_matches_the_method(dtype, nq, nkv, lens, nodes, kv_bs):
     c = Case(nq, nkv, lens, nodes, dtype, kv_bs, seed=sum(lens) + nq)
@@ -180,9 +183,10 @@ def test_chain_without_a_mask():
     c.check(*c.reference(mask=False))
 
 
-def test_rows_that_see_nothing_give_zero():
+@pytest.mark.parametrize("nkv", [2, 4])
+def test_rows_that_see_nothing_give_zero(nkv):
     # a sequence that is all drafts (no committed token), some nodes with an empty mask
-    c = Case(4, 2, [20, 50], [20, 6], torch.bfloat16, seed=7)
+    c = Case(4, nkv, [20, 50], [20, 6], torch.bfloat16, seed=7)
     c.bits[[0, 3, 19]] = False
     c.bits[[21]] = False       # sees its committed tokens only
     assert c.run() == 0
@@ -192,12 +196,13 @@ def test_rows_that_see_nothing_give_zero():
     c.check(ref, tol)
 
 
-def test_masked_draft_rows_may_hold_anything():
+@pytest.mark.parametrize("nodes", [5, 12, 40])
+def test_masked_draft_rows_may_hold_anything(nodes):
     # node 2's K and V rows hold inf and NaN; nodes that do not see it are untouched by them
-    c = Case(4, 2, [60], [5], torch.float32, seed=8)
+    c = Case(4, 2, [60], [nodes], torch.float32, seed=8)
     c.bits[:, 2] = False
     ref, tol = c.reference()
-    slot = int(c.slots[0][57])
+    slot = int(c.slots[0][60 - nodes + 2])
     c.cache.kscale[slot // 32, :, slot % 32] = float("nan")
     c.cache.vscale[slot // 32, :, slot % 32] = float("inf")
     assert c.run() == 0
@@ -222,9 +227,10 @@ def test_one_node_equals_the_decode():
     assert float((dec - c.out).abs().max()) <= 2 * tol  # both are fp32 forms of one sum
 
 
-def test_large_scores_and_v_steps():
+@pytest.mark.parametrize("nodes", [4, 8, 20])  # 16, 32, 80 rows: both kernels
+def test_large_scores_and_v_steps(nodes):
     # keys and values over many octaves: the running maximum jumps, the V steps' exponent grows
-    c = Case(8, 2, [3000], [20], torch.float32, seed=11)
+    c = Case(8, 2, [3000], [nodes], torch.float32, seed=11)
     f = torch.tensor(2.0) ** torch.randint(-20, 3, c.cache.vscale.shape)
     c.cache.vscale.mul_(f.to(DEV))
     c.cache.kscale.mul_((torch.tensor(2.0) ** torch.randint(-4, 4, c.cache.kscale.shape)).to(DEV))
@@ -232,8 +238,9 @@ def test_large_scores_and_v_steps():
     c.check(*c.reference())
 
 
-def test_long_context_many_chunks():
-    c = Case(4, 1, [20011], [11], torch.bfloat16, seed=12)
+@pytest.mark.parametrize("nodes", [3, 8, 11, 30, 60])  # 12, 32, 44, 120, 240 rows
+def test_long_context_many_chunks(nodes):
+    c = Case(4, 1, [20011], [nodes], torch.bfloat16, seed=12)
     assert c.run() == 0
     c.check(*c.reference())
     first = c.out.clone()
@@ -258,8 +265,9 @@ def test_zero_nodes_and_empty_batch():
     ([100, 50], [0, 4, 40]),     # past total_q
     ([100, 50], [0, 4, 2]),      # offsets descend
 ])
-def test_bad_sequence_is_reported_and_skipped(lens, off):
-    c = Case(4, 2, [100, 50], [4, 5], torch.float32, seed=15)
+@pytest.mark.parametrize("nq", [2, 16])
+def test_bad_sequence_is_reported_and_skipped(lens, off, nq):
+    c = Case(nq, 2, [100, 50], [4, 5], torch.float32, seed=15)
     ref, tol = c.reference()
     table = np.full((2, 7), -1, np.int32)
     table[:, :c.table.shape[1]] = c.table
@@ -271,8 +279,9 @@ def test_bad_sequence_is_reported_and_skipped(lens, off):
 
 
 @pytest.mark.parametrize("bad", [-1, 10 ** 9, "pages"])
-def test_bad_page_is_left_out(bad):
-    c = Case(4, 2, [200, 70], [4, 5], torch.float32, seed=16)
+@pytest.mark.parametrize("nq", [4, 16])
+def test_bad_page_is_left_out(bad, nq):
+    c = Case(nq, 2, [200, 70], [4, 5], torch.float32, seed=16)
     ref, tol = c.reference()
     table = c.table.copy()
     table[0, 1] = c.cache.num_pages if bad == "pages" else bad
