@@ -1,6 +1,9 @@
 // kq8_internal.h -- launchers shared between the libkq8 translation units.
 #pragma once
 
+#include <atomic>
+#include <cstdint>
+
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -54,6 +57,35 @@ int encode_tensor_map(CUtensorMap* map, CUtensorMapDataType type, uint32_t rank,
                       CUtensorMapSwizzle swizzle);
 // SMs of the current device (152 without one).
 int device_sms();
+
+// A programmatic launch of `kern` with `smem` bytes of dynamic shared memory.  The
+// opt-in to more than 48 KB is made once per kernel and device (it costs as much as
+// a launch).
+template <typename... KArgs, typename... Args>
+int launch_smem(void (*kern)(KArgs...), std::atomic<uint64_t>& opted, dim3 grid, int threads,
+                size_t smem, cudaStream_t stream, Args... args) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return KQ8_ERR_CUDA;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (!(opted.load(std::memory_order_relaxed) & bit)) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
+            cudaSuccess)
+            return KQ8_ERR_CUDA;
+        opted.fetch_or(bit, std::memory_order_relaxed);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kern, args...) != cudaSuccess) return KQ8_ERR_CUDA;
+    return cudaPeekAtLastError() == cudaSuccess ? KQ8_OK : KQ8_ERR_CUDA;
+}
 
 int launch_append(const kq8_cache_t& c, const float* k, const float* v, const int32_t* slot,
                   int32_t T, uint32_t* status, cudaStream_t stream);

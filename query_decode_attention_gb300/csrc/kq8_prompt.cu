@@ -20,7 +20,8 @@
 //                   16, both operands in shared memory) and O_t += P_t V (A in TMEM,
 //                   V read with the dimension as its major axis, so that the rows
 //                   are used as they lie in memory);
-//   warp 9          TMA loads: Q once, then K and V blocks through a ring of five.
+//   warp 9          TMA loads: Q once, then K and V blocks through a ring of five;
+//   warp 10         clears the rows of the last V block that lie behind the end.
 // Per step the order is PV_A(j), S_A(j+1), PV_B(j), S_B(j+1): one tile's scores
 // turn into weights while the other tile's products run.  MMAs of one thread
 // complete in order, so S_t(j+1) may overwrite P_t(j), and when S_t(j) has
@@ -43,7 +44,7 @@ constexpr int PR_ROWS = 128;   // rows per query tile
 constexpr int PR_BLK = 128;    // tokens per block
 constexpr int PR_RING = 5;     // K / V blocks in shared memory
 constexpr int PR_THREADS = 12 * 32;
-constexpr int PR_MMA_WARP = 8, PR_LOAD_WARP = 9;
+constexpr int PR_MMA_WARP = 8, PR_LOAD_WARP = 9, PR_TAIL_WARP = 10;
 // registers per thread: 168 at launch; the softmax warpgroups take what the
 // third one gives back (2 * 216 + 72 = 3 * 168)
 constexpr int PR_REGS_SOFTMAX = 216, PR_REGS_REST = 72;
@@ -62,10 +63,13 @@ constexpr int PB_Q = 0;          // Q has landed
 constexpr int PB_FULL = 1;       // [ring] block has landed
 constexpr int PB_EMPTY = 6;      // [ring] both tiles have used the block
 constexpr int PB_S = 11;         // [tile] commit after S_t
-constexpr int PB_P = 13;         // [tile] 4 softmax warps wrote P_t (and rescaled O_t)
-constexpr int PB_O = 15;         // [tile] commit after the last PV_t
-constexpr int PB_FINAL = 17;     // last commit, waited on before TMEM is freed
-constexpr int PB_COUNT = 18;
+constexpr int PB_P = 13;         // [tile][half] 4 softmax warps wrote 64 columns of P_t
+                                 // (and, before the first half, rescaled O_t)
+constexpr int PB_O = 17;         // [tile] commit after the last PV_t
+constexpr int PB_LAST = 19;      // the last V has landed, where rows in it are to be cleared
+constexpr int PB_TAIL = 20;      // and they are
+constexpr int PB_FINAL = 21;     // last commit, waited on before TMEM is freed
+constexpr int PB_COUNT = 22;
 
 constexpr float PR_LOG2E = 1.4426950408889634f;
 constexpr float PR_SLACK = 8.0f;
@@ -125,6 +129,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
     const int nA = lastA / PR_BLK + 1;
     const int nB = i0 + TQ < L ? lastB / PR_BLK + 1 : 0;
     const int nblk = max(nA, nB);
+    const bool tail = nblk * PR_BLK > L;  // the last block reaches behind the sequence
 
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + PR_SM_BAR);
     uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + PR_SM_TMEM);
@@ -142,13 +147,20 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tbase = *tslot;
-    // A wait that runs out is recorded and makes every later wait give up at once.
+    // A wait that runs out is recorded and makes every later wait that does not
+    // succeed at once give up.
     auto wait = [&](int i, uint32_t parity) -> bool {
-        if (*abort_flag) return false;
-        if (mbar_wait_bounded(bars + i, parity)) return true;
-        *abort_flag = 1;
-        if (P.status) atomicOr(P.status, KQ8_STATUS_TIMEOUT);
-        return false;
+        if (mbar_try_wait(bars + i, parity)) return true;
+        const long long t0 = clock64();
+        while (!mbar_try_wait(bars + i, parity)) {
+            if (*abort_flag) return false;
+            if (clock64() - t0 > (1ll << 28)) {
+                *abort_flag = 1;
+                if (P.status) atomicOr(P.status, KQ8_STATUS_TIMEOUT);
+                return false;
+            }
+        }
+        return true;
     };
 
     if (warp >= 8) {
@@ -163,14 +175,16 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                 for (int p = 0; p < 2; p++)
                     tma_load_3d(sm + PR_SM_Q + t * PR_TILE + p * PR_PANEL, &P.qmap, 64 * p, h * G,
                                 s0 + i0 + t * TQ, bars + PB_Q, pol);
-            int armed[PR_RING];
-            for (int i = 0; i < PR_RING; i++) armed[i] = -1;
-            for (int it = 0; it < 2 * nblk; it++) {
+            // the last V lands on a barrier of its own where the tail warp waits for it
+            auto landed = [&](int it) {
+                return tail && it == 2 * nblk - 1 ? PB_LAST : PB_FULL + it % PR_RING;
+            };
+            int it = 0;
+            for (; it < 2 * nblk; it++) {
                 const int s = it % PR_RING;
                 if (it >= PR_RING && !wait(PB_EMPTY + s, (it / PR_RING - 1) & 1)) break;
-                uint64_t* bar = bars + PB_FULL + s;
+                uint64_t* bar = bars + landed(it);
                 mbar_arrive_expect_tx(bar, PR_TILE);
-                armed[s] = it;
                 for (int p = 0; p < 2; p++)
                     tma_load_3d(sm + PR_SM_RING + s * PR_TILE + p * PR_PANEL,
                                 it & 1 ? &P.vmap : &P.kmap, 64 * p, h, s0 + (it >> 1) * PR_BLK, bar,
@@ -179,11 +193,10 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
             // an aborted CTA lets the copies in flight land (bounded)
             if (*abort_flag) {
                 mbar_wait_bounded(bars + PB_Q, 0);
-                for (int s = 0; s < PR_RING; s++)
-                    if (armed[s] >= 0)
-                        mbar_wait_bounded(bars + PB_FULL + s, (armed[s] / PR_RING) & 1);
+                for (int i = it > PR_RING ? it - PR_RING : 0; i < it; i++)
+                    mbar_wait_bounded(bars + landed(i), landed(i) == PB_LAST ? 0 : (i / PR_RING) & 1);
             }
-        } else if (warp == PR_MMA_WARP) {
+        } else if (warp == PR_MMA_WARP && lane == 0) {
             // ---- every MMA.  Operand rows are 128 bytes, swizzled; a K-major step of
             // 16 elements is 32 bytes along the row, V's step of 16 tokens two groups
             // of eight rows.
@@ -192,81 +205,71 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
             const uint64_t dv = tc::sdesc_sw128(smem_u32(sm + PR_SM_RING), PR_PANEL, 1024);
             constexpr uint32_t IDS = tc::IDesc<128, PR_BLK, BF16>::value;
             constexpr uint32_t IDO = tc::IDesc<128, HD, BF16>::value | tc::IDESC_B_MN;
-            auto issue_s = [&](int t, int j) {
-                if (lane == 0) {
-                    const uint64_t a = dq + (uint64_t)(t * (PR_TILE >> 4));
-                    const uint64_t k = dk + (uint64_t)((2 * j) % PR_RING * (PR_TILE >> 4));
+            auto issue_s = [&](int t, uint64_t k) {
+                const uint64_t a = dq + (uint64_t)(t * (PR_TILE >> 4));
 #pragma unroll
-                    for (int kk = 0; kk < HD / 16; kk++) {
-                        const uint64_t o = (kk >> 2) * (PR_PANEL >> 4) + (kk & 3) * 2;
-                        tc::mma_f16(tbase + 128 * t, a + o, k + o, IDS, kk > 0);
-                    }
-                    tc::mma_commit(bars + PB_S + t);
+                for (int kk = 0; kk < HD / 16; kk++) {
+                    const uint64_t o = (kk >> 2) * (PR_PANEL >> 4) + (kk & 3) * 2;
+                    tc::mma_f16(tbase + 128 * t, a + o, k + o, IDS, kk > 0);
                 }
+                tc::mma_commit(bars + PB_S + t);
             };
-            auto issue_pv = [&](int t, int j) {
-                if (lane == 0) {
-                    const uint64_t v = dv + (uint64_t)((2 * j + 1) % PR_RING * (PR_TILE >> 4));
-#pragma unroll
-                    for (int kk = 0; kk < PR_BLK / 16; kk++)
-                        tc::mma_f16_ta(tbase + PR_COL_O + 128 * t, tbase + 128 * t + 8 * kk,
-                                       v + (uint64_t)(kk * (2048 >> 4)), IDO, j > 0 || kk > 0);
-                    if (j == (t ? nB : nA) - 1) tc::mma_commit(bars + PB_O + t);
-                }
-            };
-            // a ring place is released when a later load waits for it
-            auto release = [&](int it) {
-                if (lane == 0 && it + PR_RING < 2 * nblk) tc::mma_commit(bars + PB_EMPTY + it % PR_RING);
-            };
-            auto all = [&](bool x) { return __all_sync(0xffffffffu, x) != 0; };
-            bool ok = all(wait(PB_Q, 0)) && all(wait(PB_FULL, 0));
+            bool ok = wait(PB_Q, 0) && wait(PB_FULL, 0);
             if (ok) {
                 tc::fence_after_sync();
-                issue_s(0, 0);
-                if (nB) issue_s(1, 0);
-                release(0);
+                issue_s(0, dk);
+                if (nB) issue_s(1, dk);
+                if (PR_RING < 2 * nblk) tc::mma_commit(bars + PB_EMPTY);
             }
+            // ring places (and phases) of V of block j and of K of block j + 1
+            int sv = 1, sk = 2;
+            uint32_t pv = 0, pk = 0;
             for (int j = 0; ok && j < nblk; j++) {
-                const int itv = 2 * j + 1, itk = 2 * j + 2;
-                ok = all(wait(PB_FULL + itv % PR_RING, (itv / PR_RING) & 1));
-                if (!ok) break;
-                if ((j + 1) * PR_BLK > L) {
-                    // rows behind the sequence's end belong to others: weights of 0 must
-                    // not meet what they hold
-                    uint8_t* v = sm + PR_SM_RING + (itv % PR_RING) * PR_TILE;
-                    for (int c = (L - j * PR_BLK) * 8 + lane; c < PR_BLK * 8; c += 32)
-                        for (int p = 0; p < 2; p++)
-                            *reinterpret_cast<uint4*>(v + p * PR_PANEL + c * 16) =
-                                make_uint4(0u, 0u, 0u, 0u);
-                    tc::fence_smem_to_async();
-                    __syncwarp();
-                }
-                bool have_k = false;
-                for (int t = 0; ok && t < 2; t++) {
+                const uint64_t v = dv + (uint64_t)(sv * (PR_TILE >> 4));
+                const uint64_t k = dk + (uint64_t)(sk * (PR_TILE >> 4));
+                const bool more = j + 1 < nblk;
+                ok = (tail && !more ? wait(PB_TAIL, 0) : wait(PB_FULL + sv, pv)) &&
+                     (!more || wait(PB_FULL + sk, pk));
+                for (int t = 0; ok && t < (nB ? 2 : 1); t++) {
                     const int nt = t ? nB : nA;
-                    if (j < nt) {
-                        ok = all(wait(PB_P + t, j & 1));
-                        if (!ok) break;
+                    if (j >= nt) continue;
+                    // the two halves of P as they come
+#pragma unroll
+                    for (int half = 0; half < 2; half++) {
+                        if (!(ok = ok && wait(PB_P + 2 * t + half, j & 1))) break;
                         tc::fence_after_sync();
-                        issue_pv(t, j);
+#pragma unroll
+                        for (int kk = 4 * half; kk < 4 * half + 4; kk++)
+                            tc::mma_f16_ta(tbase + PR_COL_O + 128 * t, tbase + 128 * t + 8 * kk,
+                                           v + (uint64_t)(kk * (2048 >> 4)), IDO, j > 0 || kk > 0);
                     }
-                    if (t == 1 || nB == 0) release(itv);
-                    if (j + 1 < nt) {
-                        if (!have_k) {
-                            ok = all(wait(PB_FULL + itk % PR_RING, (itk / PR_RING) & 1));
-                            if (!ok) break;
-                            tc::fence_after_sync();
-                            have_k = true;
-                        }
-                        issue_s(t, j + 1);
-                    }
-                    if ((t == 1 || nB == 0) && j + 1 < nblk) release(itk);
-                    if (nB == 0) break;
+                    if (!ok) break;
+                    if (j + 1 < nt)
+                        issue_s(t, k);
+                    else
+                        tc::mma_commit(bars + PB_O + t);
                 }
+                // a ring place is released when a later load waits for it
+                if (ok && 2 * j + 1 + PR_RING < 2 * nblk) tc::mma_commit(bars + PB_EMPTY + sv);
+                if (ok && 2 * j + 2 + PR_RING < 2 * nblk) tc::mma_commit(bars + PB_EMPTY + sk);
+                if ((sv += 2) >= PR_RING) sv -= PR_RING, pv ^= 1;
+                if ((sk += 2) >= PR_RING) sk -= PR_RING, pk ^= 1;
             }
-            if (lane == 0) {  // completes once every MMA issued above has (bounded)
-                tc::mma_commit(bars + PB_FINAL);
-                mbar_wait_bounded(bars + PB_FINAL, 0);
+            // completes once every MMA issued above has (bounded)
+            tc::mma_commit(bars + PB_FINAL);
+            mbar_wait_bounded(bars + PB_FINAL, 0);
+        } else if (warp == PR_TAIL_WARP && tail) {
+            // ---- rows behind the sequence's end belong to others: weights of 0 must not
+            // meet what they hold
+            if (__all_sync(0xffffffffu, wait(PB_LAST, 0))) {
+                uint8_t* v = sm + PR_SM_RING + ((2 * nblk - 1) % PR_RING) * PR_TILE;
+                for (int c = (L - (nblk - 1) * PR_BLK) * 8 + lane; c < PR_BLK * 8; c += 32)
+                    for (int p = 0; p < 2; p++)
+                        *reinterpret_cast<uint4*>(v + p * PR_PANEL + c * 16) =
+                            make_uint4(0u, 0u, 0u, 0u);
+                tc::fence_smem_to_async();
+                __syncwarp();
+                if (lane == 0) pr_arrive(bars + PB_TAIL);
             }
         }
     } else {
@@ -294,9 +297,13 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
 #pragma unroll
                 for (int c = 0; c < PR_BLK; c++) x[c] = c <= vis ? x[c] : -INFINITY;
             }
-            float mt = fmaxf(x[0], x[1]);
+            float m4[4] = {x[0], x[1], x[2], x[3]};  // four chains: the latency, not the issue
 #pragma unroll
-            for (int c = 2; c < PR_BLK; c += 2) mt = fmaxf(mt, fmaxf(x[c], x[c + 1]));
+            for (int c = 4; c < PR_BLK; c += 8)
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    m4[i] = fmaxf(m4[i], c + 4 + i < PR_BLK ? fmaxf(x[c + i], x[c + 4 + i]) : x[c + i]);
+            const float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
             const bool need = mt > M + slack || j == 0;
             if (j > 0 && __any_sync(0xffffffffu, need)) {
                 const float f = need ? pr_ex2((M - mt) * sl2) : 1.0f;
@@ -324,10 +331,10 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                     w[c] = __uint_as_float(pack2<BF16>(p.x, p.y));
                 }
                 tc::tmem_st32(tS + 32 * q, w);
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) pr_arrive(bars + PB_P + 2 * t + q);
             }
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) pr_arrive(bars + PB_P + t);
         }
         // ---- output after the last PV_t
         if (nt > 0 && ok && __all_sync(0xffffffffu, wait(PB_O + t, 0))) {
@@ -378,21 +385,8 @@ int row_map(CUtensorMap* map, bool bf16, const void* base, int64_t tokens, int64
 
 template <bool BF16>
 int launch_prompt(const PromptParams& p, dim3 grid, cudaStream_t s) {
-    if (cudaFuncSetAttribute(kq8_prompt_kernel<BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)PR_SMEM) != cudaSuccess)
-        return KQ8_ERR_CUDA;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(PR_THREADS);
-    cfg.dynamicSmemBytes = PR_SMEM;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kq8_prompt_kernel<BF16>, p) != cudaSuccess) return KQ8_ERR_CUDA;
-    return cudaPeekAtLastError() == cudaSuccess ? KQ8_OK : KQ8_ERR_CUDA;
+    static std::atomic<uint64_t> opted{0};
+    return launch_smem(kq8_prompt_kernel<BF16>, opted, grid, PR_THREADS, PR_SMEM, s, p);
 }
 
 }  // namespace

@@ -671,23 +671,10 @@ TreePlan tree_plan(int B, int nq, int nkv, int max_seq_len, int max_q_len) {
 
 template <int MT, bool HILO>
 int launch_tree(const TreeParams& p, dim3 grid, cudaStream_t s) {
-    constexpr size_t smem = sizeof(TreeSmem<MT>) + 1024;  // slack to round the base up
-    if (cudaFuncSetAttribute(kq8_tree_kernel<MT, HILO>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)smem) != cudaSuccess)
-        return KQ8_ERR_CUDA;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(TR_THREADS);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kq8_tree_kernel<MT, HILO>, p) != cudaSuccess) return KQ8_ERR_CUDA;
-    return cudaPeekAtLastError() == cudaSuccess ? KQ8_OK : KQ8_ERR_CUDA;
+    static std::atomic<uint64_t> opted{0};
+    return launch_smem(kq8_tree_kernel<MT, HILO>, opted, grid, TR_THREADS,
+                       sizeof(TreeSmem<MT>) + 1024,  // slack to round the base up
+                       s, p);
 }
 
 }  // namespace

@@ -182,6 +182,8 @@ class PagedKVCache:
                                    self.vscale.data_ptr(), self.num_pages, self.kv_bs,
                                    self.num_kv_heads, self.head_dim)
 
+        self.ref = ctypes.byref(self._struct)  # keeps the struct alive
+
     @property
     def struct(self) -> kq8_cache_t:
         return self._struct
@@ -521,43 +523,65 @@ def kq8_read_status(word: torch.Tensor, stream=None) -> int:
     return int(st.value)
 
 
-# ---- rows of any type and stride, draft trees ----
+# ---- rows of any type and stride, draft trees, packed prompts ----
+# These calls are made once per layer and step, so their marshalling is kept short:
+# device indices and raw pointers instead of device and stream objects.
 
-def _rows(t: torch.Tensor, name: str) -> ctypes.c_void_p:
+def _where(name: str, device: int, t: torch.Tensor, dtype=torch.int32) -> int:
+    """Pointer of a contiguous tensor of `dtype` on device `device`."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != device:
+        raise ValueError("kq8 takes CUDA tensors of one device" if t.is_cuda
+                         else "kq8 takes CUDA tensors")
+    if not t.is_contiguous():
+        raise ValueError("kq8 takes contiguous tensors")
+    return t.data_ptr()
+
+
+def _rows(name: str, device: int, t: torch.Tensor, dtype) -> int:
     """Pointer of a [tokens, heads, 128] tensor whose rows are adjacent elements."""
-    if not t.is_cuda:
-        raise ValueError("kq8 takes CUDA tensors")
-    if t.dtype not in DTYPES:
-        raise TypeError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != device:
+        raise ValueError("kq8 takes CUDA tensors of one device" if t.is_cuda
+                         else "kq8 takes CUDA tensors")
     if t.dim() != 3 or t.shape[2] != HEAD_DIM or t.stride(2) != 1:
         raise ValueError(f"{name} must be [tokens, heads, 128] with adjacent elements in a row")
     return t.data_ptr()
 
 
-def _stream_on(device: torch.device, stream, *tensors) -> ctypes.c_void_p:
-    """The stream of a call on `device`: the given one, or that device's current
-    one.  Every tensor of the call has to be there, and the device has to be the
-    current one (a launch goes to the current device)."""
-    for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"the call's tensors are on {device} and {t.device}")
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"the call's tensors are on {device}, not on the current device")
-    return _stream(stream)
+def _launch_on(device: int, stream) -> int:
+    """The raw stream of a call whose tensors are on `device`: the given one, or that
+    device's current one.  A launch goes to the current device, so it has to be that."""
+    if device < 0:
+        raise ValueError("kq8 takes CUDA tensors")
+    if device != torch.cuda.current_device():
+        raise ValueError(f"the call's tensors are on cuda:{device}, not on the current device")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _type_code(name: str, t: torch.Tensor) -> int:
+    code = DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
+    return code
 
 
 def _rows_args(cache, k, v, slot, status, stream):
-    kp, vp = _rows(k, "k"), _rows(v, "v")
-    _dtype(slot, torch.int32, "slot")
-    T, nkv = slot.numel(), cache.num_kv_heads
-    if tuple(k.shape) != (T, nkv, HEAD_DIM) or v.shape != k.shape or v.dtype != k.dtype:
-        raise ValueError("k and v must be [len(slot), nkv, 128] of one type")
-    if status is not None:
-        _dtype(status, torch.int32, "status")
-    st = _stream_on(cache.k.device, stream, k, v, slot, status)
-    sk, sv = k.stride(), v.stride()
-    return (ctypes.byref(cache.struct), cache.bits, kp, vp, DTYPES[k.dtype], sk[0], sk[1], sv[0],
-            sv[1], _ptr(slot), T, _ptr(status), st)
+    dev, dt = cache.k.get_device(), k.dtype
+    code = _type_code("k", k)
+    st = _launch_on(dev, stream)
+    kp, vp = _rows("k", dev, k, dt), _rows("v", dev, v, dt)
+    sp, T = _where("slot", dev, slot), slot.numel()
+    if k.shape != v.shape or k.shape[0] != T or k.shape[1] != cache.num_kv_heads:
+        raise ValueError("k and v must be [len(slot), nkv, 128]")
+    wp = None if status is None else _where("status", dev, status)
+    kt, kh, _ = k.stride()
+    vt, vh, _ = v.stride()
+    return cache.ref, cache.bits, kp, vp, code, kt, kh, vt, vh, sp, T, wp, st
 
 
 def kq8_write_kv(cache: PagedKVCache, k: torch.Tensor, v: torch.Tensor, slot: torch.Tensor,
@@ -565,7 +589,9 @@ def kq8_write_kv(cache: PagedKVCache, k: torch.Tensor, v: torch.Tensor, slot: to
     """Write path for k, v [T, nkv, 128] of float32, float16 or bfloat16 with any
     token and head stride, into a q8 or q4 cache; slot int32 [T]
     (include/kq8.h)."""
-    _check(_lib.kq8_write_kv(*_rows_args(cache, k, v, slot, status, stream)), "kq8_write_kv")
+    rc = _lib.kq8_write_kv(*_rows_args(cache, k, v, slot, status, stream))
+    if rc:
+        raise Kq8Error(rc, "kq8_write_kv")
 
 
 def kq8_read_kv(cache: PagedKVCache, k: torch.Tensor, v: torch.Tensor, slot: torch.Tensor,
@@ -573,7 +599,9 @@ def kq8_read_kv(cache: PagedKVCache, k: torch.Tensor, v: torch.Tensor, slot: tor
     """The values of the cache's rows at slot int32 [T] into k, v [T, nkv, 128] of
     float32, float16 or bfloat16, any strides; rows with a negative slot stay as
     they were (include/kq8.h)."""
-    _check(_lib.kq8_read_kv(*_rows_args(cache, k, v, slot, status, stream)), "kq8_read_kv")
+    rc = _lib.kq8_read_kv(*_rows_args(cache, k, v, slot, status, stream))
+    if rc:
+        raise Kq8Error(rc, "kq8_read_kv")
 
 
 def kq8_tree_workspace_bytes(B: int, nq: int, nkv: int, max_seq_len: int, max_q_len: int) -> int:
@@ -590,30 +618,31 @@ def kq8_tree_attn(out: torch.Tensor, q: torch.Tensor, cache: PagedKVCache,
     mask_words] holds each node's visible nodes as bits (None: a chain)."""
     if cache.bits != 8:
         raise ValueError("the tree attention reads a q8 cache")
-    qp = _rows(q, "q")
-    _dtype(out, q.dtype, "out")
-    _dtype(page_table, torch.int32, "page_table")
-    _dtype(seq_lens, torch.int32, "seq_lens")
-    _dtype(q_offsets, torch.int32, "q_offsets")
+    dev, dt = cache.k.get_device(), q.dtype
+    code = _type_code("q", q)
+    st = _launch_on(dev, stream)
+    qp, op = _rows("q", dev, q, dt), _where("out", dev, out, dt)
+    tp, lp = _where("page_table", dev, page_table), _where("seq_lens", dev, seq_lens)
+    fp = _where("q_offsets", dev, q_offsets)
+    total, nq, _ = q.shape
+    B = seq_lens.numel()
     if out.shape != q.shape:
         raise ValueError("q and out must be [total_q, nq, 128]")
-    B = seq_lens.numel()
     if q_offsets.numel() != B + 1 or page_table.dim() != 2 or page_table.shape[0] != B:
         raise ValueError("q_offsets must be [B+1] and page_table [B, max_pages]")
-    words = 0
+    mp, words = None, 0
     if tree_mask is not None:
-        _dtype(tree_mask, torch.int32, "tree_mask")
-        if tree_mask.dim() != 2 or tree_mask.shape[0] != q.shape[0]:
+        mp = _where("tree_mask", dev, tree_mask)
+        if tree_mask.dim() != 2 or tree_mask.shape[0] != total:
             raise ValueError("tree_mask must be [total_q, mask_words]")
         words = tree_mask.shape[1]
-    st = _stream_on(cache.k.device, stream, out, q, page_table, seq_lens, q_offsets, tree_mask,
-                    workspace)
-    _check(_lib.kq8_tree_attn(_ptr(out), qp, DTYPES[q.dtype], q.stride(0), q.stride(1), q.shape[0],
-                              ctypes.byref(cache.struct), _ptr(page_table), page_table.shape[1],
-                              _ptr(seq_lens), _ptr(q_offsets), _ptr(tree_mask), words,
-                              int(max_seq_len), int(max_q_len), B, q.shape[1], float(scale),
-                              _ptr(workspace), workspace.numel() * workspace.element_size(), st),
-           "kq8_tree_attn")
+    qt, qh, _ = q.stride()
+    rc = _lib.kq8_tree_attn(op, qp, code, qt, qh, total, cache.ref, tp, page_table.shape[1], lp, fp,
+                            mp, words, int(max_seq_len), int(max_q_len), B, nq, float(scale),
+                            _where("workspace", dev, workspace, workspace.dtype),
+                            workspace.numel() * workspace.element_size(), st)
+    if rc:
+        raise Kq8Error(rc, "kq8_tree_attn")
 
 
 def kq8_tree_commit(cache: PagedKVCache, page_table: torch.Tensor, base_lens: torch.Tensor,
@@ -622,19 +651,19 @@ def kq8_tree_commit(cache: PagedKVCache, page_table: torch.Tensor, base_lens: to
     """Moves each sequence's accepted drafts path int32 [B, max_path] (the first
     path_len[b] of a row, ascending) behind its base_lens[b] committed tokens
     (include/kq8.h)."""
-    for t, name in ((page_table, "page_table"), (base_lens, "base_lens"), (path, "path"),
-                    (path_len, "path_len")):
-        _dtype(t, torch.int32, name)
+    dev = cache.k.get_device()
+    st = _launch_on(dev, stream)
+    tp, bp = _where("page_table", dev, page_table), _where("base_lens", dev, base_lens)
+    pp, np_ = _where("path", dev, path), _where("path_len", dev, path_len)
     B = base_lens.numel()
     if (path.dim() != 2 or path.shape[0] != B or path_len.numel() != B
             or page_table.dim() != 2 or page_table.shape[0] != B):
         raise ValueError("page_table must be [B, max_pages], path [B, max_path], path_len [B]")
-    if status is not None:
-        _dtype(status, torch.int32, "status")
-    st = _stream_on(cache.k.device, stream, page_table, base_lens, path, path_len, status)
-    _check(_lib.kq8_tree_commit(ctypes.byref(cache.struct), cache.bits, _ptr(page_table),
-                                page_table.shape[1], _ptr(base_lens), _ptr(path), _ptr(path_len),
-                                path.shape[1], B, _ptr(status), st), "kq8_tree_commit")
+    wp = None if status is None else _where("status", dev, status)
+    rc = _lib.kq8_tree_commit(cache.ref, cache.bits, tp, page_table.shape[1], bp, pp, np_,
+                              path.shape[1], B, wp, st)
+    if rc:
+        raise Kq8Error(rc, "kq8_tree_commit")
 
 
 def kq8_prompt_attn(out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -643,22 +672,25 @@ def kq8_prompt_attn(out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torc
     """Causal attention over packed prompts (include/kq8.h): q and out [total, nq,
     128], k and v [total, nkv, 128] of float16 or bfloat16 (q, k, v of any token and
     head stride), cu_seqlens int32 [B+1], no sequence longer than max_len."""
-    qp, kp, vp = _rows(q, "q"), _rows(k, "k"), _rows(v, "v")
-    for t, name in ((out, "out"), (k, "k"), (v, "v")):
-        _dtype(t, q.dtype, name)
-    _dtype(cu_seqlens, torch.int32, "cu_seqlens")
+    dev, dt = q.get_device(), q.dtype
+    code = _type_code("q", q)
+    st = _launch_on(dev, stream)
+    op, qp = _where("out", dev, out, dt), _rows("q", dev, q, dt)
+    kp, vp = _rows("k", dev, k, dt), _rows("v", dev, v, dt)
+    cp, B = _where("cu_seqlens", dev, cu_seqlens), cu_seqlens.numel() - 1
     if out.shape != q.shape or k.shape != v.shape or k.shape[0] != q.shape[0]:
         raise ValueError("q and out must be [total, nq, 128], k and v [total, nkv, 128]")
-    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+    if B < 0 or cu_seqlens.dim() != 1:
         raise ValueError("cu_seqlens must be [B+1]")
-    if status is not None:
-        _dtype(status, torch.int32, "status")
-    st = _stream_on(q.device, stream, out, k, v, cu_seqlens, status)
-    sq, sk, sv = q.stride(), k.stride(), v.stride()
-    _check(_lib.kq8_prompt_attn(_ptr(out), qp, kp, vp, DTYPES[q.dtype], sq[0], sq[1], sk[0], sk[1],
-                                sv[0], sv[1], _ptr(cu_seqlens), q.shape[0], int(max_len),
-                                cu_seqlens.numel() - 1, q.shape[1], k.shape[1], float(scale),
-                                _ptr(status), st), "kq8_prompt_attn")
+    wp = None if status is None else _where("status", dev, status)
+    qt, qh, _ = q.stride()
+    kt, kh, _ = k.stride()
+    vt, vh, _ = v.stride()
+    total, nq, _ = q.shape
+    rc = _lib.kq8_prompt_attn(op, qp, kp, vp, code, qt, qh, kt, kh, vt, vh, cp, total,
+                              int(max_len), B, nq, k.shape[1], float(scale), wp, st)
+    if rc:
+        raise Kq8Error(rc, "kq8_prompt_attn")
 
 
 # ---- test-only exports -------------------------------------------------------
