@@ -13,21 +13,25 @@
 // Roles (three warpgroups, which meet on mbarriers only):
 //   warps 0-3, 4-7  softmax of tile A, B, one thread per row (TMEM lane): the 128
 //                   scores of a block in registers, the running maximum and sum in
-//                   fp32, the weights p = 2^(x - m) back to TMEM as 16-bit pairs
-//                   over the scores they came from; O is rescaled in place only
-//                   when the maximum grows by more than 2^8;
-//   warp 8          one lane issues every MMA: S_t = Q_t K^T (8 of M = N = 128, K =
-//                   16, both operands in shared memory) and O_t += P_t V (A in TMEM,
-//                   V read with the dimension as its major axis, so that the rows
-//                   are used as they lie in memory);
-//   warp 9          TMA loads: Q once, then K and V blocks through a ring of five;
-//   warp 10         clears the rows of the last V block that lie behind the end.
-// Per step the order is PV_A(j), S_A(j+1), PV_B(j), S_B(j+1): one tile's scores
-// turn into weights while the other tile's products run.  MMAs of one thread
-// complete in order, so S_t(j+1) may overwrite P_t(j), and when S_t(j) has
-// arrived PV_t(j-1) is in O_t.
-// What bounds it: 16 MMAs of 128 x 128 x 16 per tile and block, 8192 FLOP per
-// cycle and SM at best, against 16384 exponentials in the same time.
+//                   fp32, the weights p = 2^(x - m) back to TMEM as 16-bit pairs; O is
+//                   rescaled in place only when the maximum grows by more than 2^8;
+//   warp 8          one lane issues S = Q_t K^T, the tiles in turn (8 MMAs of M = N =
+//                   128, K = 16, both operands in shared memory);
+//   warps 9, 11     one lane each issues O_t += P_t V of tile A, B (A in TMEM, V read
+//                   with the dimension as its major axis, so that the rows are used as
+//                   they lie in memory);
+//   warp 10         TMA loads: Q once, then K and V blocks through a ring of five; at
+//                   the end it clears the rows of the last V block that lie behind the
+//                   sequence.
+// TMEM holds O of both tiles (2 x 128 columns), the weights of both (2 x 64) and one
+// block of scores (128) that the tiles use in turn: a row's scores are in registers a
+// few hundred cycles after their product, so the next product of the other tile, and
+// then the tile's own next one, run beside the softmax instead of behind it.  (With
+// the weights over their own scores, and so S_t(j+1) behind PV_t(j), a step took 3780
+// cycles against 2048 of MMAs.)
+// What bounds it: 16 MMAs of 128 x 128 x 16 per tile and block, 8192 FLOP per cycle and
+// SM at best (64 cycles each, measured), against 16384 exponentials per tile in the
+// same time (4 cycles a warp and sub-partition, measured).
 #include <cstdint>
 #include <cstring>
 
@@ -44,14 +48,14 @@ constexpr int PR_ROWS = 128;   // rows per query tile
 constexpr int PR_BLK = 128;    // tokens per block
 constexpr int PR_RING = 5;     // K / V blocks in shared memory
 constexpr int PR_THREADS = 12 * 32;
-constexpr int PR_MMA_WARP = 8, PR_LOAD_WARP = 9, PR_TAIL_WARP = 10;
+constexpr int PR_S_WARP = 8, PR_PVA_WARP = 9, PR_LOAD_WARP = 10, PR_PVB_WARP = 11;
 // registers per thread: 168 at launch; the softmax warpgroups take what the
 // third one gives back (2 * 216 + 72 = 3 * 168)
 constexpr int PR_REGS_SOFTMAX = 216, PR_REGS_REST = 72;
 constexpr uint32_t PR_PANEL = PR_ROWS * 128;   // 128 rows x 64 16-bit elements
 constexpr uint32_t PR_TILE = 2 * PR_PANEL;     // 128 rows x 128 elements
-// TMEM columns: S_t (P_t over its first 64) at 128 t, O_t at 256 + 128 t
-constexpr uint32_t PR_COLS = 512, PR_COL_O = 256;
+// TMEM columns: O_t at 128 t, S at 256, P_t at 384 + 64 t
+constexpr uint32_t PR_COLS = 512, PR_COL_S = 256, PR_COL_P = 384;
 // shared memory: Q tiles, ring, barriers
 constexpr uint32_t PR_SM_Q = 0, PR_SM_RING = 2 * PR_TILE;
 constexpr uint32_t PR_SM_BAR = PR_SM_RING + PR_RING * PR_TILE;
@@ -60,16 +64,22 @@ constexpr uint32_t PR_SMEM = PR_SM_ABORT + 4 + 1024;  // slack to round the base
 static_assert(PR_SMEM <= 232448, "shared memory of one CTA");
 
 constexpr int PB_Q = 0;          // Q has landed
+// The ring's length is odd, so K(j) takes the place of V(j-3), and V(j) that of K(j-2).
+// The S thread waits for K's phases of a place only, the PV threads for V's; a parity
+// wait is sound as the phase in between has completed by then: before S(j) the tiles
+// have read S(j-1), so they had finished P(j-2), for which PV(j-3) was done; before
+// PV(j) a PV thread has seen P(j-1), which came of S(j-1) behind S(j-2).
 constexpr int PB_FULL = 1;       // [ring] block has landed
 constexpr int PB_EMPTY = 6;      // [ring] both tiles have used the block
-constexpr int PB_S = 11;         // [tile] commit after S_t
-constexpr int PB_P = 13;         // [tile][half] 4 softmax warps wrote 64 columns of P_t
+constexpr int PB_S = 11;         // [tile] commit after S of the tile
+constexpr int PB_SR = 13;        // 4 softmax warps hold S in registers (the tiles in turn)
+constexpr int PB_P = 14;         // [tile][half] 4 softmax warps wrote 64 columns of P_t
                                  // (and, before the first half, rescaled O_t)
-constexpr int PB_O = 17;         // [tile] commit after the last PV_t
-constexpr int PB_LAST = 19;      // the last V has landed, where rows in it are to be cleared
-constexpr int PB_TAIL = 20;      // and they are
-constexpr int PB_FINAL = 21;     // last commit, waited on before TMEM is freed
-constexpr int PB_COUNT = 22;
+constexpr int PB_PV = 18;        // [tile] commit after PV_t
+constexpr int PB_LAST = 20;      // the last V has landed, where rows in it are to be cleared
+constexpr int PB_TAIL = 21;      // and they are
+constexpr int PB_FINAL = 22;     // [MMA thread] last commit, waited on before TMEM is freed
+constexpr int PB_COUNT = 25;
 
 constexpr float PR_LOG2E = 1.4426950408889634f;
 constexpr float PR_SLACK = 8.0f;
@@ -139,7 +149,14 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
         tc::tmem_alloc(tslot, PR_COLS);
     }
     if (tid == 0) {
-        for (int i = 0; i < PB_COUNT; i++) mbar_init(bars + i, i >= PB_P && i < PB_O ? 4 : 1);
+        for (int i = 0; i < PB_COUNT; i++) {
+            uint32_t cnt = 1;
+            // V is released by a PV thread per tile, K by the S thread, which arrives for
+            // both: the ring's length is odd, so K and V take a place in turn
+            if (i >= PB_EMPTY && i < PB_S) cnt = nB ? 2 : 1;
+            if (i >= PB_SR && i < PB_PV) cnt = 4;
+            mbar_init(bars + i, cnt);
+        }
         *abort_flag = 0;
         fence_barrier_init();
     }
@@ -165,103 +182,43 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
 
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(PR_REGS_REST));
-        if (warp == PR_LOAD_WARP && lane == 0) {
-            // ---- loads: ring item 2 j is K of block j, 2 j + 1 its V
-            const uint64_t pol = l2_evict_first_policy();
-            const uint64_t keep = l2_evict_last_policy();
-            const uint32_t qbytes = (uint32_t)(TQ * G) * 128u;
-            mbar_arrive_expect_tx(bars + PB_Q, 2 * qbytes * (nB ? 2 : 1));
-            for (int t = 0; t < (nB ? 2 : 1); t++)
-                for (int p = 0; p < 2; p++)
-                    tma_load_3d(sm + PR_SM_Q + t * PR_TILE + p * PR_PANEL, &P.qmap, 64 * p, h * G,
-                                s0 + i0 + t * TQ, bars + PB_Q, pol);
-            // the last V lands on a barrier of its own where the tail warp waits for it
-            auto landed = [&](int it) {
-                return tail && it == 2 * nblk - 1 ? PB_LAST : PB_FULL + it % PR_RING;
-            };
-            int it = 0;
-            for (; it < 2 * nblk; it++) {
-                const int s = it % PR_RING;
-                if (it >= PR_RING && !wait(PB_EMPTY + s, (it / PR_RING - 1) & 1)) break;
-                uint64_t* bar = bars + landed(it);
-                mbar_arrive_expect_tx(bar, PR_TILE);
-                for (int p = 0; p < 2; p++)
-                    tma_load_3d(sm + PR_SM_RING + s * PR_TILE + p * PR_PANEL,
-                                it & 1 ? &P.vmap : &P.kmap, 64 * p, h, s0 + (it >> 1) * PR_BLK, bar,
-                                keep);
-            }
-            // an aborted CTA lets the copies in flight land (bounded)
-            if (*abort_flag) {
-                mbar_wait_bounded(bars + PB_Q, 0);
-                for (int i = it > PR_RING ? it - PR_RING : 0; i < it; i++)
-                    mbar_wait_bounded(bars + landed(i), landed(i) == PB_LAST ? 0 : (i / PR_RING) & 1);
-            }
-        } else if (warp == PR_MMA_WARP && lane == 0) {
-            // ---- every MMA.  Operand rows are 128 bytes, swizzled; a K-major step of
-            // 16 elements is 32 bytes along the row, V's step of 16 tokens two groups
-            // of eight rows.
-            const uint64_t dq = tc::sdesc_sw128(smem_u32(sm + PR_SM_Q), 16, 1024);
-            const uint64_t dk = tc::sdesc_sw128(smem_u32(sm + PR_SM_RING), 16, 1024);
-            const uint64_t dv = tc::sdesc_sw128(smem_u32(sm + PR_SM_RING), PR_PANEL, 1024);
-            constexpr uint32_t IDS = tc::IDesc<128, PR_BLK, BF16>::value;
-            constexpr uint32_t IDO = tc::IDesc<128, HD, BF16>::value | tc::IDESC_B_MN;
-            auto issue_s = [&](int t, uint64_t k) {
-                const uint64_t a = dq + (uint64_t)(t * (PR_TILE >> 4));
-#pragma unroll
-                for (int kk = 0; kk < HD / 16; kk++) {
-                    const uint64_t o = (kk >> 2) * (PR_PANEL >> 4) + (kk & 3) * 2;
-                    tc::mma_f16(tbase + 128 * t, a + o, k + o, IDS, kk > 0);
+        if (warp == PR_LOAD_WARP) {
+            if (lane == 0) {
+                // ---- loads: ring item 2 j is K of block j, 2 j + 1 its V
+                const uint64_t pol = l2_evict_first_policy();
+                const uint64_t keep = l2_evict_last_policy();
+                const uint32_t qbytes = (uint32_t)(TQ * G) * 128u;
+                mbar_arrive_expect_tx(bars + PB_Q, 2 * qbytes * (nB ? 2 : 1));
+                for (int t = 0; t < (nB ? 2 : 1); t++)
+                    for (int p = 0; p < 2; p++)
+                        tma_load_3d(sm + PR_SM_Q + t * PR_TILE + p * PR_PANEL, &P.qmap, 64 * p, h * G,
+                                    s0 + i0 + t * TQ, bars + PB_Q, pol);
+                // the last V lands on a barrier of its own where the tail warp waits for it
+                auto landed = [&](int it) {
+                    return tail && it == 2 * nblk - 1 ? PB_LAST : PB_FULL + it % PR_RING;
+                };
+                int it = 0;
+                for (; it < 2 * nblk; it++) {
+                    const int s = it % PR_RING;
+                    if (it >= PR_RING && !wait(PB_EMPTY + s, (it / PR_RING - 1) & 1)) break;
+                    uint64_t* bar = bars + landed(it);
+                    mbar_arrive_expect_tx(bar, PR_TILE);
+                    for (int p = 0; p < 2; p++)
+                        tma_load_3d(sm + PR_SM_RING + s * PR_TILE + p * PR_PANEL,
+                                    it & 1 ? &P.vmap : &P.kmap, 64 * p, h, s0 + (it >> 1) * PR_BLK, bar,
+                                    keep);
                 }
-                tc::mma_commit(bars + PB_S + t);
-            };
-            bool ok = wait(PB_Q, 0) && wait(PB_FULL, 0);
-            if (ok) {
-                tc::fence_after_sync();
-                issue_s(0, dk);
-                if (nB) issue_s(1, dk);
-                if (PR_RING < 2 * nblk) tc::mma_commit(bars + PB_EMPTY);
-            }
-            // ring places (and phases) of V of block j and of K of block j + 1
-            int sv = 1, sk = 2;
-            uint32_t pv = 0, pk = 0;
-            for (int j = 0; ok && j < nblk; j++) {
-                const uint64_t v = dv + (uint64_t)(sv * (PR_TILE >> 4));
-                const uint64_t k = dk + (uint64_t)(sk * (PR_TILE >> 4));
-                const bool more = j + 1 < nblk;
-                ok = (tail && !more ? wait(PB_TAIL, 0) : wait(PB_FULL + sv, pv)) &&
-                     (!more || wait(PB_FULL + sk, pk));
-                for (int t = 0; ok && t < (nB ? 2 : 1); t++) {
-                    const int nt = t ? nB : nA;
-                    if (j >= nt) continue;
-                    // the two halves of P as they come
-#pragma unroll
-                    for (int half = 0; half < 2; half++) {
-                        if (!(ok = ok && wait(PB_P + 2 * t + half, j & 1))) break;
-                        tc::fence_after_sync();
-#pragma unroll
-                        for (int kk = 4 * half; kk < 4 * half + 4; kk++)
-                            tc::mma_f16_ta(tbase + PR_COL_O + 128 * t, tbase + 128 * t + 8 * kk,
-                                           v + (uint64_t)(kk * (2048 >> 4)), IDO, j > 0 || kk > 0);
-                    }
-                    if (!ok) break;
-                    if (j + 1 < nt)
-                        issue_s(t, k);
-                    else
-                        tc::mma_commit(bars + PB_O + t);
+                // an aborted CTA lets the copies in flight land (bounded)
+                if (*abort_flag) {
+                    mbar_wait_bounded(bars + PB_Q, 0);
+                    for (int i = it > PR_RING ? it - PR_RING : 0; i < it; i++)
+                        mbar_wait_bounded(bars + landed(i), landed(i) == PB_LAST ? 0 : (i / PR_RING) & 1);
                 }
-                // a ring place is released when a later load waits for it
-                if (ok && 2 * j + 1 + PR_RING < 2 * nblk) tc::mma_commit(bars + PB_EMPTY + sv);
-                if (ok && 2 * j + 2 + PR_RING < 2 * nblk) tc::mma_commit(bars + PB_EMPTY + sk);
-                if ((sv += 2) >= PR_RING) sv -= PR_RING, pv ^= 1;
-                if ((sk += 2) >= PR_RING) sk -= PR_RING, pk ^= 1;
             }
-            // completes once every MMA issued above has (bounded)
-            tc::mma_commit(bars + PB_FINAL);
-            mbar_wait_bounded(bars + PB_FINAL, 0);
-        } else if (warp == PR_TAIL_WARP && tail) {
-            // ---- rows behind the sequence's end belong to others: weights of 0 must not
-            // meet what they hold
-            if (__all_sync(0xffffffffu, wait(PB_LAST, 0))) {
+            __syncwarp();
+            if (tail && __all_sync(0xffffffffu, wait(PB_LAST, 0))) {
+                // rows behind the sequence's end belong to others: weights of 0 must not
+                // meet what they hold
                 uint8_t* v = sm + PR_SM_RING + ((2 * nblk - 1) % PR_RING) * PR_TILE;
                 for (int c = (L - (nblk - 1) * PR_BLK) * 8 + lane; c < PR_BLK * 8; c += 32)
                     for (int p = 0; p < 2; p++)
@@ -271,6 +228,72 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                 __syncwarp();
                 if (lane == 0) pr_arrive(bars + PB_TAIL);
             }
+        } else if (warp == PR_S_WARP && lane == 0) {
+            // ---- S of both tiles, in turn.  Operand rows are 128 bytes, swizzled; a
+            // K-major step of 16 elements is 32 bytes along the row.
+            const uint64_t dq = tc::sdesc_sw128(smem_u32(sm + PR_SM_Q), 16, 1024);
+            const uint64_t dk = tc::sdesc_sw128(smem_u32(sm + PR_SM_RING), 16, 1024);
+            constexpr uint32_t IDS = tc::IDesc<128, PR_BLK, BF16>::value;
+            bool ok = wait(PB_Q, 0);
+            int place = 0;
+            uint32_t phase = 0, read = 0;  // of K of block j; S blocks issued so far
+            for (int j = 0; ok && j < nblk; j++) {
+                const uint64_t k = dk + (uint64_t)(place * (PR_TILE >> 4));
+                ok = wait(PB_FULL + place, phase);
+                for (int t = 0; ok && t < 2; t++) {
+                    if (j >= (t ? nB : nA)) continue;
+                    // the scores before these are in registers
+                    if (read > 0 && !(ok = wait(PB_SR, (read - 1) & 1))) break;
+                    read++;
+                    tc::fence_after_sync();
+                    const uint64_t a = dq + (uint64_t)(t * (PR_TILE >> 4));
+#pragma unroll
+                    for (int kk = 0; kk < HD / 16; kk++) {
+                        const uint64_t o = (kk >> 2) * (PR_PANEL >> 4) + (kk & 3) * 2;
+                        tc::mma_f16(tbase + PR_COL_S, a + o, k + o, IDS, kk > 0);
+                    }
+                    tc::mma_commit(bars + PB_S + t);
+                }
+                // a ring place is released when a later load waits for it
+                if (ok && 2 * j + PR_RING < 2 * nblk) {
+                    tc::mma_commit(bars + PB_EMPTY + place);
+                    if (nB) pr_arrive(bars + PB_EMPTY + place);
+                }
+                if ((place += 2) >= PR_RING) place -= PR_RING, phase ^= 1;
+            }
+            tc::mma_commit(bars + PB_FINAL);  // completes once every MMA above has (bounded)
+            mbar_wait_bounded(bars + PB_FINAL, 0);
+        } else if ((warp == PR_PVA_WARP || (warp == PR_PVB_WARP && nB)) && lane == 0) {
+            // ---- PV of tile t.  V's step of 16 tokens is two groups of eight rows.
+            const int t = warp == PR_PVB_WARP ? 1 : 0, nt = t ? nB : nA;
+            const uint64_t dv = tc::sdesc_sw128(smem_u32(sm + PR_SM_RING), PR_PANEL, 1024);
+            constexpr uint32_t IDO = tc::IDesc<128, HD, BF16>::value | tc::IDESC_B_MN;
+            const uint32_t tO = tbase + 128 * t, tP = tbase + PR_COL_P + 64 * t;
+            bool ok = true;
+            int place = 1;
+            uint32_t phase = 0;
+            for (int j = 0; ok && j < nt; j++) {
+                const uint64_t v = dv + (uint64_t)(place * (PR_TILE >> 4));
+                ok = tail && j + 1 == nblk ? wait(PB_TAIL, 0) : wait(PB_FULL + place, phase);
+                // the two halves of P as they come
+#pragma unroll
+                for (int half = 0; half < 2; half++) {
+                    if (!(ok = ok && wait(PB_P + 2 * t + half, j & 1))) break;
+                    tc::fence_after_sync();
+#pragma unroll
+                    for (int kk = 4 * half; kk < 4 * half + 4; kk++)
+                        tc::mma_f16_ta(tO, tP + 8 * kk, v + (uint64_t)(kk * (2048 >> 4)), IDO,
+                                       j > 0 || kk > 0);
+                }
+                if (!ok) break;
+                tc::mma_commit(bars + PB_PV + t);
+                // (tile B sees at most one block more than tile A, and no later load waits
+                // for the places of the last two blocks)
+                if (2 * j + 1 + PR_RING < 2 * nblk) tc::mma_commit(bars + PB_EMPTY + place);
+                if ((place += 2) >= PR_RING) place -= PR_RING, phase ^= 1;
+            }
+            tc::mma_commit(bars + PB_FINAL + 1 + t);
+            mbar_wait_bounded(bars + PB_FINAL + 1 + t, 0);
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(PR_REGS_SOFTMAX));
@@ -280,7 +303,8 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
         const bool valid = row < TQ * G && tok < L;
         const int first = i0 + t * TQ;          // the tile's first token
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t tS = tbase + 128 * t + lanes, tO = tbase + PR_COL_O + 128 * t + lanes;
+        const uint32_t tS = tbase + PR_COL_S + lanes, tO = tbase + 128 * t + lanes;
+        const uint32_t tP = tbase + PR_COL_P + 64 * t + lanes;
         const float sl2 = P.scale * PR_LOG2E;
         const float slack = PR_SLACK / sl2;
         float M = -INFINITY;  // reference of the weights, in units of raw scores
@@ -292,6 +316,9 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
             tc::fence_after_sync();
             float x[PR_BLK];
             tc::tmem_ld_cols<PR_BLK>(tS, x);
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) pr_arrive(bars + PB_SR);
             if ((j + 1) * PR_BLK - 1 > first) {  // a diagonal block: token c sees 0 .. tok
                 const int vis = tok - j * PR_BLK;  // last visible column
 #pragma unroll
@@ -305,6 +332,12 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                     m4[i] = fmaxf(m4[i], c + 4 + i < PR_BLK ? fmaxf(x[c + i], x[c + 4 + i]) : x[c + i]);
             const float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
             const bool need = mt > M + slack || j == 0;
+            // PV_t of the block before has read P_t and is in O_t
+            if (j > 0) {
+                ok = __all_sync(0xffffffffu, wait(PB_PV + t, (j - 1) & 1));
+                if (!ok) break;
+                tc::fence_after_sync();
+            }
             if (j > 0 && __any_sync(0xffffffffu, need)) {
                 const float f = need ? pr_ex2((M - mt) * sl2) : 1.0f;
                 sum = __fmul2_rn(sum, make_float2(f, f));
@@ -330,14 +363,14 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                     sum = __fadd2_rn(sum, p);
                     w[c] = __uint_as_float(pack2<BF16>(p.x, p.y));
                 }
-                tc::tmem_st32(tS + 32 * q, w);
+                tc::tmem_st32(tP + 32 * q, w);
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) pr_arrive(bars + PB_P + 2 * t + q);
             }
         }
         // ---- output after the last PV_t
-        if (nt > 0 && ok && __all_sync(0xffffffffu, wait(PB_O + t, 0))) {
+        if (nt > 0 && ok && __all_sync(0xffffffffu, wait(PB_PV + t, (nt - 1) & 1))) {
             tc::fence_after_sync();
             const float inv = __fdiv_rn(1.0f, sum.x + sum.y);
             uint4* dst = reinterpret_cast<uint4*>(
