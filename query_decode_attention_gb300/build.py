@@ -19,7 +19,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libkq8.so")
 
 SOURCES = ["kq8_attn.cu", "kq8_sparse.cu", "kq8_misc.cu", "kq8_api.cu", "kq8_prefill.cu",
-           "kq8_rows.cu", "kq8_tree.cu", "kq8_prompt.cu"]
+           "kq8_rows.cu", "kq8_tree.cu", "kq8_tree_tc.cu",
+           "kq8_prompt.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "-I" + INCLUDE,
               "-I" + CSRC]

@@ -30,97 +30,14 @@
 // eight V rows of a transposed 8 x 8 load are tok(i, 0..7): all different
 // modulo 8, so the 128-byte swizzle keeps that load free of conflicts too.
 // The weights therefore go from accumulators to operands within the lane.
-#include <cuda_bf16.h>
-
 #include <cstring>
 #include <type_traits>
 
-#include "kq8_common.cuh"
 #include "kq8_internal.h"
+#include "kq8_tree.cuh"
 
 namespace kq8 {
 namespace {
-
-constexpr float TR_LOG2E = 1.4426950408889634f;
-constexpr size_t TR_STATUS_BYTES = 256;
-constexpr size_t TR_COUNTERS = 16384;
-constexpr size_t TR_HEADER = TR_STATUS_BYTES + TR_COUNTERS * sizeof(uint32_t);
-
-struct TreeParams {
-    CUtensorMap vmap;
-    void* out;
-    const void* q;
-    int64_t q_st, q_sh;  // element strides of q's tokens and heads
-    int32_t dtype;
-    int32_t total_q;
-    kq8_cache_t cache;
-    const int32_t* page_table;
-    int32_t max_pages;
-    const int32_t* seq_lens;
-    const int32_t* q_off;
-    const uint32_t* mask;  // [total_q][mask_words]; null: node i sees nodes 0 .. i
-    int32_t mask_words;
-    int32_t max_seq_len, max_q_len;
-    int32_t b0;            // first sequence of this launch
-    int32_t nq, G;
-    float scale;
-    int32_t chunk_tiles, num_chunks, row_tiles;
-    float* part_acc;       // [pairs][tile's rows][num_chunks][HD]
-    float2* part_ms;       // [pairs][tile's rows][num_chunks]
-    uint32_t* status;
-    uint32_t* counters;    // [pairs]
-};
-
-__device__ __forceinline__ float tr_ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// 4 elements of a q row as fp32 (exact).
-__device__ __forceinline__ float4 load_q4(const void* q, int dtype, int64_t at) {
-    if (dtype == KQ8_F32) return *reinterpret_cast<const float4*>(static_cast<const float*>(q) + at);
-    const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(q) + at);
-    if (dtype == KQ8_F16) {
-        const float2 a = h2_to_f2(w.x), b = h2_to_f2(w.y);
-        return make_float4(a.x, a.y, b.x, b.y);
-    }
-    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u),
-                       __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u));
-}
-// One rounding to the output type.
-__device__ __forceinline__ void store_out4(void* out, int dtype, size_t at, const float4 x) {
-    if (dtype == KQ8_F32) {
-        *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = x;
-    } else if (dtype == KQ8_F16) {
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) =
-            make_uint2(f2_to_h2(x.x, x.y), f2_to_h2(x.z, x.w));
-    } else {
-        __nv_bfloat162 a = __floats2bfloat162_rn(x.x, x.y), b = __floats2bfloat162_rn(x.z, x.w);
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) =
-            make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
-    }
-}
-
-// What node i of a sequence with nb nodes sees among nodes jt .. jt + 31, as
-// bits; a negative node index is a committed token (always seen), one past the
-// last node never is.
-__device__ __forceinline__ uint32_t node_window(const TreeParams& P, int64_t row0, int i, int nb,
-                                                int jt) {
-    auto word = [&](int w) -> uint32_t {
-        if (w < 0) return 0xFFFFFFFFu;
-        const int j0 = 32 * w;
-        if (j0 >= nb) return 0u;
-        uint32_t x;
-        if (P.mask)
-            x = P.mask[(row0 + i) * P.mask_words + w];
-        else
-            x = i >= j0 + 31 ? 0xFFFFFFFFu : (i < j0 ? 0u : (2u << (i - j0)) - 1u);
-        return nb >= j0 + 32 ? x : x & ((1u << (nb - j0)) - 1u);
-    };
-    const int w = jt >> 5, s = jt & 31;  // floor division
-    return __funnelshift_r(word(w), s ? word(w + 1) : 0u, s);
-}
 
 constexpr int TR_WARPS = 4;
 constexpr int TR_THREADS = TR_WARPS * 32;
@@ -615,7 +532,8 @@ __global__ void __launch_bounds__(TR_THREADS, TreeShape<MT>::CTAS)
 // A call's split: rows of a tile, sequences per launch (so that the tickets of a
 // launch fit the header's counters), row tiles, chunks and the partials' places.
 struct TreePlan {
-    int tile_rows = 16;
+    int tile_rows = 16;  // 16, 32: kq8_tree_kernel; 128, 256: the tensor cores
+    int ctas = 0;        // of the tensor cores' kernel
     int seqs = 0, row_tiles = 1, chunk_tiles = TR_WARPS, num_chunks = 1;
     size_t off_ms = 0, off_acc = 0, total = TR_HEADER;
 };
@@ -644,24 +562,35 @@ int64_t tree_chunk(int64_t pairs, int64_t tiles, int ctas_per_sm) {
     return best;
 }
 
-TreePlan tree_plan(int B, int nq, int nkv, int max_seq_len, int max_q_len) {
+TreePlan tree_plan(int B, int nq, int nkv, int max_seq_len, int max_q_len, bool hilo) {
     TreePlan p;
     const int64_t rows = (int64_t)max_q_len * (nq / nkv);
-    p.tile_rows = rows <= 16 ? 16 : 32;
+    p.tile_rows = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 128 || hilo ? 128 : 256;
     p.row_tiles = (int)((rows + p.tile_rows - 1) / p.tile_rows);
     if (p.row_tiles < 1) p.row_tiles = 1;
     const int64_t per_seq = (int64_t)nkv * p.row_tiles;
-    if (per_seq > (int64_t)TR_COUNTERS) return p;  // seqs = 0: unsupported
-    p.seqs = (int)((int64_t)TR_COUNTERS / per_seq);
-    if (p.seqs > B) p.seqs = B;
-    const int64_t pairs = (int64_t)p.seqs * per_seq;
     const int64_t tiles = ((int64_t)max_seq_len + TILE - 1) / TILE;
-    int64_t c = tree_chunk(pairs, tiles, p.tile_rows == 16 ? TreeShape<1>::CTAS : TreeShape<2>::CTAS);
     const int64_t part = (int64_t)p.tile_rows * (HD * sizeof(float) + sizeof(float2));
-    while (c < tiles && pairs * ((tiles + c - 1) / c) * part > TR_PARTS) c *= 2;
-    p.chunk_tiles = (int)c;
-    p.num_chunks = tiles > 0 ? (int)((tiles + c - 1) / c) : 1;
-    const size_t parts = p.num_chunks > 1 ? (size_t)(pairs * p.tile_rows * p.num_chunks) : 0;
+    size_t parts = 0;
+    if (p.tile_rows <= 32) {
+        if (per_seq > (int64_t)TR_COUNTERS) return p;  // seqs = 0: unsupported
+        p.seqs = (int)((int64_t)TR_COUNTERS / per_seq);
+        if (p.seqs > B) p.seqs = B;
+        const int64_t pairs = (int64_t)p.seqs * per_seq;
+        int64_t c =
+            tree_chunk(pairs, tiles, p.tile_rows == 16 ? TreeShape<1>::CTAS : TreeShape<2>::CTAS);
+        while (c < tiles && pairs * ((tiles + c - 1) / c) * part > TR_PARTS) c *= 2;
+        p.chunk_tiles = (int)c;
+        p.num_chunks = tiles > 0 ? (int)((tiles + c - 1) / c) : 1;
+        if (p.num_chunks > 1) parts = (size_t)(pairs * p.tile_rows * p.num_chunks);
+    } else {
+        // one CTA per SM, at least two steps each; two parts a CTA
+        p.seqs = B;
+        const int64_t steps = (tiles + 3) / 4 * per_seq * B;
+        p.ctas = device_sms();
+        if ((steps + 1) / 2 < p.ctas) p.ctas = steps > 1 ? (int)((steps + 1) / 2) : 1;
+        parts = (size_t)p.ctas * 2 * p.tile_rows;
+    }
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     p.off_ms = TR_HEADER;
     p.off_acc = up(p.off_ms + parts * sizeof(float2));
@@ -687,7 +616,9 @@ extern "C" {
 size_t kq8_tree_workspace_bytes(int32_t B, int32_t nq, int32_t nkv, int32_t max_seq_len,
                                 int32_t max_q_len) {
     if (B < 0 || nq < 1 || nkv < 1 || nq % nkv || max_seq_len < 0 || max_q_len < 0) return 0;
-    return tree_plan(B, nq, nkv, max_seq_len, max_q_len).total;
+    const size_t a = tree_plan(B, nq, nkv, max_seq_len, max_q_len, false).total;
+    const size_t b = tree_plan(B, nq, nkv, max_seq_len, max_q_len, true).total;
+    return a > b ? a : b;
 }
 
 int kq8_tree_attn(void* out, const void* q, int32_t dtype, size_t q_token_stride,
@@ -709,7 +640,7 @@ int kq8_tree_attn(void* out, const void* q, int32_t dtype, size_t q_token_stride
     if (max_seq_len >= (1 << 29) || B > 65535 || nkv > 65535 || max_q_len > KQ8_TREE_MAX_NODES)
         return KQ8_ERR_UNSUPPORTED;
     if (tree_mask && (int64_t)mask_words * 32 < max_q_len) return KQ8_ERR_INVALID_ARG;
-    const TreePlan plan = tree_plan(B, nq, nkv, max_seq_len, max_q_len);
+    const TreePlan plan = tree_plan(B, nq, nkv, max_seq_len, max_q_len, dtype != KQ8_BF16);
     if (!workspace || (uintptr_t)workspace % 256 != 0 || workspace_bytes < plan.total)
         return KQ8_ERR_WORKSPACE;
     if (B == 0 || max_q_len == 0) return KQ8_OK;
@@ -756,7 +687,10 @@ int kq8_tree_attn(void* out, const void* q, int32_t dtype, size_t q_token_stride
     for (p.b0 = 0; p.b0 < B; p.b0 += plan.seqs) {
         const int seqs = B - p.b0 < plan.seqs ? B - p.b0 : plan.seqs;
         const dim3 grid((unsigned)(plan.num_chunks * plan.row_tiles), (unsigned)nkv, (unsigned)seqs);
-        if (plan.tile_rows == 16)
+        p.seqs = seqs;
+        if (plan.ctas)
+            rc = launch_tree_tc(p, plan.tile_rows, plan.ctas, st);
+        else if (plan.tile_rows == 16)
             rc = hilo ? launch_tree<1, true>(p, grid, st) : launch_tree<1, false>(p, grid, st);
         else
             rc = hilo ? launch_tree<2, true>(p, grid, st) : launch_tree<2, false>(p, grid, st);

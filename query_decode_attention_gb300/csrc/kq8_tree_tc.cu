@@ -1,0 +1,818 @@
+// kq8_tree_tc.cu -- draft-tree attention for more rows (nodes x query heads of a KV
+// head) than the 16- and 32-row kernel's matrix instructions carry well, on the
+// 5th-generation tensor cores.
+//
+// Each row is computed as in kq8_tree.cu, up to 128 rows to a tile (MMA M, TMEM lanes):
+//   S [128 rows x 128 tokens] = Q K^T      O [128 rows x 128 dims] += P V.
+// Q's rows are the method's codes times their block scales, as fp16 with a power of two
+// per row that puts the row's largest near 2^13; K's and V's codes are exact in fp16;
+// the weights p * vstep enter as fp16.  bf16 outputs (whose own rounding is 2^-9) take Q
+// and P at 11 bits, the others as hi and lo parts (22 bits), each an MMA of its own.
+//
+// What bounds it.  Per 128-token step shared memory carries the raw bytes in and out of
+// the ring (66 KB), the widened operands in (64 KB) and, per tile, Q and K (64 KB) and V
+// (32 KB) to the MMAs: 226 KB for one tile, 322 KB for two or for hi and lo, 1770 and
+// 2520 cycles at 128 bytes; the MMAs themselves take 1024 and 2048 (64 each), HBM 1440
+// for the step's 33 KB.  With few rows the mma.sync kernel moves less: see tree_plan.
+//
+// One persistent CTA per SM takes an equal share of all steps: the lists (row tile, KV
+// head, sequence) lie one behind the other and are cut where a share ends, so ragged
+// lengths leave no SM without work.  A list inside one share goes straight to the
+// output, the pieces of a cut one to a merge kernel.  Two streams of steps keep the
+// tensor core and the softmax busy at once: with two tiles (T = 2) each tile is a
+// stream; with one, the even steps are one stream and the odd steps the other, each
+// with its own O, reference and sum, joined at a list's end.  With hi and lo parts there
+// is one stream (TMEM: O 128 columns, S 2 x 128, P 128), else TMEM holds O 2 x 128, S 128
+// for both in turn, P 2 x 64.  Roles, which meet on mbarriers:
+//   warps 0-3, 4-7  softmax of stream 0, 1, one thread per row (TMEM lane), as in
+//                   kq8_prompt.cu; the reference m refers to weights (score + log2 of
+//                   the V step), so that they fit fp16 whatever the V steps are;
+//   warps 8-11      widen one 32-token sub-tile each of a step to fp16, K then V;
+//   warp 12         one lane issues S, the streams in turn;
+//   warps 13, 14    one lane each issues PV of stream 0, 1;
+//   warp 15         copies raw sub-tiles (codes and scales) into a ring.
+// Order of tokens.  Row r of a 32-token sub-tile's operands holds K position rho(r)
+// (bits 1 and 2 swapped), token krow(rho(r)): with it the copies from the raw tile
+// (contiguous 512 bytes an instruction) to the swizzled operand rows are free of bank
+// conflicts on both sides.
+#include "kq8_internal.h"
+#include "kq8_quant.cuh"
+#include "kq8_tc.cuh"
+#include "kq8_tree.cuh"
+
+namespace kq8 {
+namespace {
+
+constexpr int TC_STEP = 128;                     // tokens per step
+constexpr int TC_THREADS = 16 * 32;
+constexpr int TC_W_WIDEN = 8, TC_W_S = 12, TC_W_PV = 13, TC_W_LOAD = 15;
+// registers per thread, 128 at launch: 2 * 184 + 80 + 64 = 4 * 128
+constexpr int TC_REGS_SOFTMAX = 184, TC_REGS_WIDEN = 80, TC_REGS_REST = 64;
+constexpr uint32_t TC_PANEL = TC_STEP * 128;     // 128 rows x 64 fp16
+constexpr uint32_t TC_OP = 2 * TC_PANEL;         // an operand: 128 rows x 128 fp16
+constexpr float TC_M_INIT = -1e30f;              // reference of a row that saw nothing
+constexpr float TC_TOP = 15.0f, TC_AIM = 7.0f;   // weights stay below 2^15, are set to 2^7
+
+template <int T, bool HILO>
+struct TcShape {
+    static_assert(T == 1 || !HILO, "hi and lo parts of one tile");
+    static constexpr int NR = 128 * T;                 // rows of a list
+    static constexpr int NS = HILO ? 1 : 2;            // streams
+    // Rings, as far as shared memory goes.  A parity wait is only sound for a waiter
+    // that waits for every phase of a barrier, in order: so the raw ring is a multiple
+    // of the four widening warps long (a place has one consumer), and with one tile and
+    // two streams V has two places, one per stream (stream = step % 2).
+    static constexpr int RAWN = 8, VB = T == 1 && !HILO ? 2 : 1;
+    static constexpr uint32_t Q = 0, K = (T + (HILO ? 1 : 0)) * TC_OP, V = K + TC_OP,
+                              RAW = V + VB * TC_OP,
+                              SC = RAW + RAWN * STAGE_BYTES,  // [4][3][128] floats
+                              META = SC + 4 * 3 * 512,        // [4][4] (missing, largest log2 V step)
+                              RF = META + 4 * 4 * 8,          // [T][128] row factors
+                              EX = RF + T * 512,              // [2][128] (m, sum)
+                              MISC = EX + 2048,               // TMEM, abort, flags, share
+                              BAR = MISC + 128, SMEM = BAR + 512 + 1024;
+    // barriers
+    static constexpr int B_RAWF = 0, B_RAWE = B_RAWF + RAWN, B_KF = B_RAWE + RAWN, B_KE = B_KF + 1,
+                         B_VF = B_KE + 1, B_VE = B_VF + VB, B_SCF = B_VE + VB,
+                         B_SF = B_SCF + 4,   // [stream], hi and lo: [S buffer]
+                         B_SR = B_SF + 2,    // S is in registers: [0], hi and lo: [S buffer]
+                         B_P = B_SR + 2,     // [stream][half]
+                         B_PV = B_P + 4,     // [stream]
+                         B_QF = B_PV + 2, B_XF = B_QF + 1, B_XE = B_XF + 1,
+                         B_FINAL = B_XE + 1, B_COUNT = B_FINAL + 3;
+    static_assert(B_COUNT * 8 <= 512 && SMEM <= 232448 && RAWN % 4 == 0, "shape");
+};
+
+__device__ __forceinline__ int tc_rho(int r) { return (r & ~6) | ((r & 2) << 1) | ((r & 4) >> 1); }
+
+// 8 int8 codes -> 8 fp16, exactly.
+__device__ __forceinline__ uint4 widen8(uint32_t a, uint32_t b) {
+    const uint32_t u = a ^ 0x80808080u, v = b ^ 0x80808080u;
+    return make_uint4(hsub2(__byte_perm(u, 0x64646464u, 0x4140), 0x64806480u),
+                      hsub2(__byte_perm(u, 0x64646464u, 0x4342), 0x64806480u),
+                      hsub2(__byte_perm(v, 0x64646464u, 0x4140), 0x64806480u),
+                      hsub2(__byte_perm(v, 0x64646464u, 0x4342), 0x64806480u));
+}
+__device__ __forceinline__ void tc_arrive(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// A call's lists and the CTAs' shares of their steps.  Sequence b has lists of
+// seq_steps(b) steps, one for each KV head and row tile that holds a node; global
+// step numbers run over row tiles, then heads, then sequences.
+struct TcSeq {
+    int n, base, nb, q0, steps, row_tiles;
+    bool bad;
+};
+__device__ __forceinline__ TcSeq tc_seq(const TreeParams& P, int b, int NR) {
+    TcSeq s;
+    s.n = __ldg(P.seq_lens + b);
+    s.q0 = __ldg(P.q_off + b);
+    s.nb = __ldg(P.q_off + b + 1) - s.q0;
+    s.bad = s.n < 0 || s.n > P.max_seq_len || s.nb < 0 || s.nb > s.n || s.nb > P.max_q_len ||
+            s.q0 < 0 || (int64_t)s.q0 + s.nb > P.total_q;
+    s.base = s.n - s.nb;
+    s.steps = s.bad || s.nb == 0 ? 0 : (s.n + TC_STEP - 1) / TC_STEP;
+    s.row_tiles = s.steps ? (s.nb * P.G + NR - 1) / NR : 0;
+    return s;
+}
+// Where a CTA's share begins (in steps from the start of sequence b) and how long
+// it is.  One warp, all lanes; every CTA reads all lengths.
+struct TcShare {
+    int64_t begin, end, total;  // global steps of the share, of all lists
+    int64_t at;                 // the share's first step, counted from sequence b's first
+    int b;
+};
+__device__ __forceinline__ int64_t tc_bound(int64_t total, int c, int ctas) {
+    return total / ctas * c + total % ctas * c / ctas;
+}
+__device__ __forceinline__ TcShare tc_share(const TreeParams& P, int NR, int c, int ctas) {
+    const int lane = threadIdx.x & 31, nkv = P.cache.num_kv_heads;
+    auto seq_work = [&](int b) -> int64_t {
+        if (b >= P.b0 + P.seqs) return 0;
+        const TcSeq s = tc_seq(P, b, NR);
+        return (int64_t)s.steps * s.row_tiles * nkv;
+    };
+    TcShare r;
+    int64_t sum = 0;
+    for (int b = P.b0 + lane; b < P.b0 + P.seqs; b += 32) sum += seq_work(b);
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    r.total = sum;
+    r.begin = tc_bound(sum, c, ctas);
+    r.end = tc_bound(sum, c + 1, ctas);
+    r.b = P.b0;
+    r.at = 0;
+    int64_t before = 0;  // steps of the sequences before this round's
+    for (int b0 = P.b0; b0 < P.b0 + P.seqs && r.begin < r.end; b0 += 32) {
+        const int64_t w = seq_work(b0 + lane);
+        int64_t upto = w;  // inclusive
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += x;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, before + upto > r.begin);
+        if (past) {
+            const int l = __ffs(past) - 1;
+            const int64_t first = __shfl_sync(0xffffffffu, before + upto - w, l);
+            r.b = b0 + l;
+            r.at = r.begin - first;
+            break;
+        }
+        before += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    return r;
+}
+
+// The pieces of a share, one list at a time; every role walks the same ones.
+struct TcItem {
+    TcSeq s;
+    int b, h, rt;
+    int step0, steps;  // this piece's steps of the list's s.steps
+    __device__ bool whole() const { return steps == s.steps; }
+};
+struct TcWalk {
+    int64_t left, at;
+    int b, last_b;
+    __device__ TcWalk(const TreeParams& P, const TcShare& sh)
+        : left(sh.end - sh.begin), at(sh.at), b(sh.b), last_b(P.b0 + P.seqs) {}
+    __device__ bool next(const TreeParams& P, int NR, TcItem& it) {
+        if (left <= 0) return false;
+        for (;;) {
+            if (b >= last_b) return false;  // (does not happen: left counts real steps)
+            it.s = tc_seq(P, b, NR);
+            const int64_t work = (int64_t)it.s.steps * it.s.row_tiles * P.cache.num_kv_heads;
+            if (at < work) break;
+            at -= work;
+            b++;
+        }
+        const int list = (int)(at / it.s.steps);
+        it.b = b;
+        it.rt = list % it.s.row_tiles;
+        it.h = list / it.s.row_tiles;
+        it.step0 = (int)(at % it.s.steps);
+        it.steps = (int)min((int64_t)(it.s.steps - it.step0), left);
+        left -= it.steps;
+        at += it.steps;
+        return true;
+    }
+};
+
+template <int T, bool HILO>
+__global__ void __launch_bounds__(TC_THREADS, 1)
+    kq8_tree_tc_kernel(const __grid_constant__ TreeParams P) {
+    using Sh = TcShape<T, HILO>;
+    constexpr int NR = Sh::NR, NS = Sh::NS, RAWN = Sh::RAWN, VB = Sh::VB;
+    constexpr bool SPLIT = T == 1 && !HILO;  // the streams are the even and the odd steps
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int nkv = P.cache.num_kv_heads, kv_bs = P.cache.kv_bs, subs = kv_bs / TILE;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Sh::BAR);
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + Sh::MISC);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + Sh::MISC + 4);
+    volatile int* sub_ok = reinterpret_cast<volatile int*>(sm + Sh::MISC + 16);  // [raw place]
+    if (warp == 0) {
+        __syncwarp();
+        tc::tmem_alloc(tslot, 512);
+    }
+    if (tid == 0) {
+        for (int i = 0; i < Sh::B_COUNT; i++) {
+            uint32_t cnt = 1;
+            if (i == Sh::B_KF || (i >= Sh::B_VF && i < Sh::B_VE)) cnt = 4;
+            if (i >= Sh::B_VE && i < Sh::B_SCF) cnt = T;  // a PV thread per tile
+            if (i >= Sh::B_SCF && i < Sh::B_SF) cnt = 4;
+            if (i >= Sh::B_SR && i < Sh::B_PV) cnt = 4;   // SR and P
+            if (i >= Sh::B_QF && i < Sh::B_FINAL) cnt = 4 * NS;
+            mbar_init(bars + i, cnt);
+        }
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    // nothing is read or written before the kernel before this one has completed
+    griddep_wait();
+    griddep_launch_dependents();
+    TcShare* share_sm = reinterpret_cast<TcShare*>(sm + Sh::MISC + 64);
+    if (warp == 1) {
+        const TcShare sh = tc_share(P, NR, blockIdx.x, gridDim.x);
+        if (lane == 0) *share_sm = sh;
+    }
+    if (blockIdx.x == 0 && warp >= 2)  // bad sequences are reported once
+        for (int b = P.b0 + tid - 64; b < P.b0 + P.seqs; b += TC_THREADS - 64)
+            if (tc_seq(P, b, NR).bad) atomicOr(P.status, KQ8_STATUS_BAD_SEQLEN);
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tbase = *tslot;
+    TcWalk walk(P, *share_sm);
+    TcItem it;
+    // A wait that runs out is recorded and makes every later wait that does not
+    // succeed at once give up.
+    auto wait = [&](int i, uint32_t parity) -> bool {
+        if (mbar_try_wait(bars + i, parity)) return true;
+        const long long t0 = clock64();
+        while (!mbar_try_wait(bars + i, parity)) {
+            if (*abort_flag) return false;
+            if (clock64() - t0 > (1ll << 28)) {
+                *abort_flag = 1;
+                atomicOr(P.status, KQ8_STATUS_TIMEOUT);
+                atomicOr(P.status + 1, 1u);  // the merge leaves every split row as it was
+                return false;
+            }
+        }
+        return true;
+    };
+    auto all = [](bool x) { return __all_sync(0xffffffffu, x) != 0; };
+    float* sc = reinterpret_cast<float*>(sm + Sh::SC);
+    float2* meta = reinterpret_cast<float2*>(sm + Sh::META);
+    float* rf_sm = reinterpret_cast<float*>(sm + Sh::RF);
+    // TMEM columns
+    auto col_o = [&](int t) { return tbase + 128 * t; };
+    auto col_s = [&](uint32_t n) { return tbase + (HILO ? 128 + 128 * (n & 1) : 256); };
+    auto col_p = [&](int t) { return tbase + 384 + 64 * t; };  // hi and lo: 384, 448
+
+    if (warp >= TC_W_S) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(TC_REGS_REST));
+        if (warp == TC_W_LOAD) {
+            // ---- raw sub-tiles; a step always has four (past the end: empty).  Lanes
+            // 4 i .. 4 i + 3 issue the copies of the step's sub-tile i: K, V and the two
+            // ranges of maxima
+            const uint64_t pol = P.row_tiles > 1 ? l2_evict_last_policy() : l2_evict_first_policy();
+            const int i = (lane >> 2) & 3, piece = lane & 3;
+            uint32_t ri = 0;  // running sub-tile
+            bool ok = true;
+            while (ok && walk.next(P, NR, it)) {
+                const int tile0 = 4 * it.step0;
+                const int tiles = min(4 * it.steps, (it.s.n + TILE - 1) / TILE - tile0);
+                auto window = [&](int w) -> int32_t {  // page ids, one per lane
+                    const int t = 32 * w + lane;
+                    if (t >= tiles) return -1;
+                    const int32_t pg =
+                        P.page_table[(size_t)it.b * P.max_pages + (tile0 + t) / subs];
+                    if (pg >= 0 && pg < P.cache.num_pages) return pg;
+                    atomicOr(P.status, KQ8_STATUS_BAD_PAGE);
+                    return -1;
+                };
+                int32_t cur = window(0), nxt = window(1);
+                for (int t = 0; t < 4 * it.steps; t += 4, ri += 4) {
+                    const int s = (ri + i) % RAWN;
+                    if (ri >= (uint32_t)RAWN) {
+                        ok = __all_sync(0xffffffffu, wait(Sh::B_RAWE + s, (ri / RAWN - 1) & 1));
+                        if (!ok) break;
+                    }
+                    if ((t & 31) == 0 && t > 0) {
+                        cur = nxt;
+                        nxt = window((t >> 5) + 1);
+                    }
+                    const int32_t pg = __shfl_sync(0xffffffffu, cur, (t & 31) + i);
+                    uint64_t* bar = bars + Sh::B_RAWF + s;
+                    if (lane < 16 && piece == 0) {
+                        sub_ok[s] = pg >= 0;
+                        mbar_arrive_expect_tx(bar, pg >= 0 ? STAGE_BYTES : 0);
+                    }
+                    __syncwarp();
+                    if (lane < 16 && pg >= 0) {
+                        const int sub = (tile0 + t + i) % subs;
+                        const size_t kvo = kv_sub_off(pg, it.h, nkv, kv_bs, sub);
+                        const size_t so = scale_sub_off(pg, it.h, nkv, kv_bs, sub);
+                        const void* src = piece == 0   ? (const void*)(P.cache.k + kvo)
+                                          : piece == 1 ? (const void*)(P.cache.v + kvo)
+                                          : piece == 2 ? (const void*)(P.cache.kscale + so)
+                                                       : (const void*)(P.cache.vscale + so);
+                        const uint32_t at = piece == 0   ? 0
+                                            : piece == 1 ? SUB_K_BYTES
+                                            : piece == 2 ? SUB_K_BYTES + SUB_V_BYTES
+                                                         : SUB_K_BYTES + SUB_V_BYTES + SUB_S_BYTES;
+                        bulk_g2s(sm + Sh::RAW + s * STAGE_BYTES + at, src,
+                                 piece < 2 ? SUB_K_BYTES : SUB_S_BYTES, bar, pol);
+                    }
+                    __syncwarp();
+                }
+            }
+            // every copy has landed before shared memory is given up (bounded)
+            for (uint32_t k = ri > (uint32_t)RAWN ? ri - RAWN : 0; k < ri; k++)
+                mbar_wait_bounded(bars + Sh::B_RAWF + k % RAWN, (k / RAWN) & 1);
+        } else if (warp == TC_W_S && lane == 0) {
+            // ---- S.  Operand rows are 128 bytes, swizzled; a K-major step of 16 elements
+            // is 32 bytes along the row.
+            const uint64_t dq = tc::sdesc_sw128(smem_u32(sm + Sh::Q), 16, 1024);
+            const uint64_t dk = tc::sdesc_sw128(smem_u32(sm + Sh::K), 16, 1024);
+            constexpr uint32_t IDS = tc::IDesc<128, TC_STEP, false>::value;
+            uint32_t g = 0, n = 0, qn = 0;  // steps, products, lists so far
+            bool ok = true;
+            while (ok && walk.next(P, NR, it)) {
+                ok = wait(Sh::B_QF, qn++ & 1);
+                for (int j = 0; ok && j < it.steps; j++, g++) {
+                    if (!(ok = wait(Sh::B_KF, g & 1))) break;
+                    for (int t = 0; ok && t < T; t++, n++) {
+                        // the scores there before are in registers
+                        if (HILO) {
+                            if (n >= 2 && !(ok = wait(Sh::B_SR + (n & 1), ((n - 2) >> 1) & 1))) break;
+                        } else if (n >= 1 && !(ok = wait(Sh::B_SR, (n - 1) & 1))) {
+                            break;
+                        }
+                        tc::fence_after_sync();
+#pragma unroll
+                        for (int part = 0; part < (HILO ? 2 : 1); part++) {
+                            const uint64_t a = dq + (uint64_t)((t + part) * (TC_OP >> 4));
+#pragma unroll
+                            for (int kk = 0; kk < HD / 16; kk++) {
+                                const uint64_t o = (kk >> 2) * (TC_PANEL >> 4) + (kk & 3) * 2;
+                                tc::mma_f16(col_s(n), a + o, dk + o, IDS, kk > 0 || part > 0);
+                            }
+                        }
+                        tc::mma_commit(bars + Sh::B_SF + (HILO ? n & 1 : SPLIT ? g & 1 : t));
+                    }
+                    if (ok) tc::mma_commit(bars + Sh::B_KE);
+                }
+            }
+            // every commit has arrived before the CTA may end (bounded)
+            tc::mma_commit(bars + Sh::B_FINAL);
+            mbar_wait_bounded(bars + Sh::B_FINAL, 0);
+            if (ok && g > 0) mbar_wait_bounded(bars + Sh::B_KE, (g - 1) & 1);
+        } else if (warp >= TC_W_PV && warp < TC_W_PV + NS && lane == 0) {
+            // ---- PV of stream t.  V's step of 16 tokens is two groups of eight rows.
+            const int t = warp - TC_W_PV;
+            const uint64_t dv = tc::sdesc_sw128(smem_u32(sm + Sh::V), TC_PANEL, 1024);
+            constexpr uint32_t IDO = tc::IDesc<128, HD, false>::value | tc::IDESC_B_MN;
+            uint32_t g = 0, n = 0;  // steps, this stream's steps so far
+            bool ok = true;
+            while (ok && walk.next(P, NR, it)) {
+                bool first = true;
+                for (int j = 0; ok && j < it.steps; j++, g++) {
+                    if (SPLIT && (int)(g & 1) != t) continue;
+                    const int place = SPLIT ? t : 0;
+                    const uint64_t v = dv + (uint64_t)(place * (TC_OP >> 4));
+                    ok = wait(Sh::B_VF + place, (SPLIT ? g >> 1 : g) & 1);
+#pragma unroll
+                    for (int half = 0; half < 2; half++) {
+                        if (!(ok = ok && wait(Sh::B_P + 2 * t + half, n & 1))) break;
+                        tc::fence_after_sync();
+#pragma unroll
+                        for (int kk = 4 * half; kk < 4 * half + 4; kk++) {
+                            const uint64_t b = v + (uint64_t)(kk * (2048 >> 4));
+                            tc::mma_f16_ta(col_o(t), col_p(t) + 8 * kk, b, IDO, !first || kk > 0);
+                            if (HILO) tc::mma_f16_ta(col_o(t), col_p(1) + 8 * kk, b, IDO, true);
+                        }
+                    }
+                    if (!ok) break;
+                    first = false;
+                    n++;
+                    tc::mma_commit(bars + Sh::B_PV + t);
+                    tc::mma_commit(bars + Sh::B_VE + place);
+                }
+            }
+            tc::mma_commit(bars + Sh::B_FINAL + 1 + t);
+            mbar_wait_bounded(bars + Sh::B_FINAL + 1 + t, 0);
+            if (ok && n > 0) mbar_wait_bounded(bars + Sh::B_VE + (SPLIT ? t : 0), (n - 1) & 1);
+        }
+    } else if (warp >= TC_W_WIDEN) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(TC_REGS_WIDEN));
+        const int w = warp - TC_W_WIDEN;  // sub-tile of a step
+        const float kmul = inv127() * P.scale * TR_LOG2E;
+        uint32_t g = 0;
+        bool ok = true;
+        while (ok && walk.next(P, NR, it)) {
+            for (int j = 0; j < it.steps; j++, g++) {
+                const uint32_t ri = 4 * g + w;
+                const int s = ri % RAWN;
+                if (!(ok = all(wait(Sh::B_RAWF + s, (ri / RAWN) & 1)))) break;
+                const uint8_t* st = sm + Sh::RAW + s * STAGE_BYTES;
+                uint4 x[8];
+                {
+                    // K: lane = (position pair, 16-byte half); its 16 codes are chunks c, c + 1
+                    // of the row's panel
+#pragma unroll
+                    for (int i = 0; i < 8; i++)
+                        x[i] = *reinterpret_cast<const uint4*>(st + 512 * i + 16 * lane);
+                    const int t = krow(tc_rho(lane));
+                    const float* rs = reinterpret_cast<const float*>(st + SUB_K_BYTES + SUB_V_BYTES);
+                    const bool have = sub_ok[s] != 0;
+                    const bool live = have && (4 * (it.step0 + j) + w) * TILE + t < it.s.n;
+                    const float ks = rs[t], vs = rs[32 + t];
+                    if (g > 0 && !(ok = all(wait(Sh::B_KE, (g - 1) & 1)))) break;
+                    // a token past the end or on a missing page counts for nothing.  (The
+                    // multipliers' place was last read for step g - 4.  S(g - 1), which freed
+                    // K's place, was issued when the scores before it had been read, by
+                    // streams that had therefore begun step g - 3 or a later one of theirs.)
+                    float* d = sc + (g & 3) * 384 + 32 * w + lane;
+                    const float vstep = live ? __fmul_rn(vs, inv127()) : 0.0f;
+                    float lv;  // log2 of the V step, from below; what is not finite does not count
+                    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(lv) : "f"(vstep));
+                    lv = lv < 128.0f ? fmaxf(lv, -90.0f) : -90.0f;
+                    d[0] = live ? __fmul_rn(ks, kmul) : 0.0f;
+                    d[128] = vstep;
+                    d[256] = lv;
+                    const float top = warp_max(lv);
+                    if (lane == 0) meta[(g & 3) * 4 + w] = make_float2(have ? 0.0f : 1.0f, top);
+                    uint8_t* dst = sm + Sh::K;
+#pragma unroll
+                    for (int i = 0; i < 8; i++) {
+                        const int blk = i >> 1, row = 32 * w + tc_rho((i & 1) * 16 + (lane >> 1));
+                        const int c = (blk & 1) * 4 + (lane & 1) * 2;
+                        uint8_t* o = dst + (blk >> 1) * TC_PANEL + row * 128;
+                        *reinterpret_cast<uint4*>(o + ((c ^ (row & 7)) << 4)) =
+                            widen8(x[i].x, x[i].y);
+                        *reinterpret_cast<uint4*>(o + (((c + 1) ^ (row & 7)) << 4)) =
+                            widen8(x[i].z, x[i].w);
+                    }
+                    tc::fence_smem_to_async();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tc_arrive(bars + Sh::B_SCF + (g & 3));
+                        tc_arrive(bars + Sh::B_KF);
+                    }
+                }
+                // V: tokens t and t + 4 (neighbouring positions), one panel each
+                const int a = (lane >> 2) & 1, q = lane & 3, p = a ^ ((lane >> 3) & 1);
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    const int pi = 2 * i + (lane >> 4);
+                    const int t = (pi >> 2) * 8 + (pi & 3) + 4 * a;
+                    x[i] = *reinterpret_cast<const uint4*>(st + SUB_K_BYTES + t * HD + 64 * p + 16 * q);
+                }
+                // the raw place is given back as soon as its bytes are in registers
+                __syncwarp();
+                if (lane == 0) tc_arrive(bars + Sh::B_RAWE + s);
+                const int place = VB == 2 ? g & 1 : 0;
+                if (g >= (uint32_t)VB && !(ok = all(wait(Sh::B_VE + place, (g / VB - 1) & 1)))) break;
+                uint8_t* dst = sm + Sh::V + place * TC_OP;
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    const int pi = 2 * i + (lane >> 4);
+                    const int t = (pi >> 2) * 8 + (pi & 3) + 4 * a;
+                    const int row = 32 * w + tc_rho(kpos(t));
+                    uint8_t* o = dst + p * TC_PANEL + row * 128;
+                    *reinterpret_cast<uint4*>(o + (((2 * q) ^ (row & 7)) << 4)) =
+                        widen8(x[i].x, x[i].y);
+                    *reinterpret_cast<uint4*>(o + (((2 * q + 1) ^ (row & 7)) << 4)) =
+                        widen8(x[i].z, x[i].w);
+                }
+                tc::fence_smem_to_async();
+                __syncwarp();
+                if (lane == 0) tc_arrive(bars + Sh::B_VF + place);
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(TC_REGS_SOFTMAX));
+        const int t = warp >> 2, w4 = warp & 3;  // stream
+        const int row = w4 * 32 + lane;          // of its tile
+        const uint32_t lanes = (uint32_t)(w4 * 32) << 16;
+        const uint32_t tO = col_o(t) + lanes, tP = col_p(t) + lanes;
+        float2* ex = reinterpret_cast<float2*>(sm + Sh::EX);
+        uint32_t g = 0, n = 0, xn = 0;  // steps, this stream's steps, lists so far
+        bool ok = t < NS;
+        for (int piece = 0; ok && walk.next(P, NR, it); piece++) {
+            const int tile = T == 2 ? t : 0;
+            const int r0 = it.rt * NR + 128 * tile;        // first row of the tile
+            const int rows = it.s.nb * P.G - r0;           // of the tile (may be <= 0 or > 128)
+            // ---- Q (article 9-2 §2 seg. 1): codes times block scales, scaled per row.
+            // Stream t of a split tile prepares half of it.  (With one tile the streams
+            // have met since their last scores, below.)
+            constexpr int QR = SPLIT ? 16 : 32;            // rows per warp
+#pragma unroll 4
+            for (int i = 0; i < QR; i++) {
+                const int r = (SPLIT ? 64 * t : 0) + w4 * QR + i;
+                float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (r < rows)
+                    x = load_q4(P.q, P.dtype, (int64_t)(it.s.q0 + (r0 + r) / P.G) * P.q_st +
+                                                  (it.h * P.G + (r0 + r) % P.G) * P.q_sh + 4 * lane);
+                float qs;
+                const uint32_t code = quantize_q_lane(x, qs);
+                float top = qs;
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                // 127 * top in [2^13, 2^14) after the scale
+                const int e = min(max((int)(__float_as_uint(top) >> 23) - 127 + 7 - 13, -100), 100);
+                if (lane == 0) rf_sm[128 * tile + r] = pow2i(e);
+                qs *= pow2i(-e);
+                float v[4];
+#pragma unroll
+                for (int k = 0; k < 4; k++) v[k] = (float)(int8_t)(code >> (8 * k)) * qs;
+                const uint2 hi = make_uint2(f2_to_h2(v[0], v[1]), f2_to_h2(v[2], v[3]));
+                uint8_t* o = sm + Sh::Q + tile * TC_OP + (lane >> 4) * TC_PANEL + r * 128 +
+                             ((((lane & 15) >> 1) ^ (r & 7)) << 4) + (lane & 1) * 8;
+                *reinterpret_cast<uint2*>(o) = hi;
+                if (HILO) {
+                    const float2 a = h2_to_f2(hi.x), b = h2_to_f2(hi.y);
+                    *reinterpret_cast<uint2*>(o + TC_OP) =
+                        make_uint2(f2_to_h2(v[0] - a.x, v[1] - a.y), f2_to_h2(v[2] - b.x, v[3] - b.y));
+                }
+            }
+            tc::fence_smem_to_async();
+            __syncwarp();
+            if (lane == 0) tc_arrive(bars + Sh::B_QF);
+            // the row factors of both streams' halves (and, in time, O's readers below)
+            if (!(ok = all(wait(Sh::B_QF, xn & 1)))) break;
+            const float rf = rf_sm[128 * tile + row];
+            const int node = (r0 + row) / P.G;
+            float M = TC_M_INIT;
+            float2 sum = make_float2(0.0f, 0.0f);
+            bool first = true;
+            for (int j = 0; ok && j < it.steps; j++, g++) {
+                if (SPLIT && (int)(g & 1) != t) continue;
+                const float* km = sc + (g & 3) * 384;
+                ok = all(wait(Sh::B_SCF + (g & 3), (g >> 2) & 1));
+                const uint32_t sn = HILO ? n >> 1 : n;
+                ok = ok && all(wait(Sh::B_SF + (HILO ? n & 1 : t), sn & 1));
+                if (!ok) break;
+                tc::fence_after_sync();
+                float x[TC_STEP];
+                tc::tmem_ld_cols<TC_STEP>(col_s(n) + lanes, x);
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) tc_arrive(bars + Sh::B_SR + (HILO ? n & 1 : 0));
+                // scores (base 2) over the row's factor
+#pragma unroll
+                for (int c = 0; c < TC_STEP; c += 4) {
+                    const float4 k4 = *reinterpret_cast<const float4*>(km + c);
+                    const float2 a = __fmul2_rn(make_float2(x[c], x[c + 1]), make_float2(k4.x, k4.y));
+                    const float2 b =
+                        __fmul2_rn(make_float2(x[c + 2], x[c + 3]), make_float2(k4.z, k4.w));
+                    x[c] = a.x;
+                    x[c + 1] = a.y;
+                    x[c + 2] = b.x;
+                    x[c + 3] = b.y;
+                }
+                const int tile0 = 4 * (it.step0 + j);  // the step's first sub-tile
+                float2 mt[4];
+                bool gone = false;
+                float lvtop = -90.0f;
+#pragma unroll
+                for (int w = 0; w < 4; w++) {
+                    mt[w] = meta[(g & 3) * 4 + w];
+                    gone |= mt[w].x != 0.0f;
+                    lvtop = fmaxf(lvtop, mt[w].y);
+                }
+                const bool masked = (tile0 + 4) * TILE > it.s.base || gone;
+                float far;  // a bound of the row's weights' exponents
+                if (masked) {
+                    // what the row sees, 32 tokens to a word
+                    far = -INFINITY;
+                    const float* lv = km + 256;
+#pragma unroll
+                    for (int w = 0; w < 4; w++) {
+                        uint32_t win = 0u;
+                        if (row < rows && mt[w].x == 0.0f)
+                            win = node_window(P, it.s.q0, node, it.s.nb, (tile0 + w) * TILE - it.s.base);
+#pragma unroll
+                        for (int c = 0; c < 32; c++) {
+                            const bool on = (win >> krow(tc_rho(c))) & 1u;
+                            x[32 * w + c] = on ? x[32 * w + c] : -INFINITY;
+                            far = fmaxf(far, fmaf(x[32 * w + c], rf, lv[32 * w + c]));
+                        }
+                    }
+                } else {
+                    float m4[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+                    for (int c = 4; c < TC_STEP; c += 8)
+#pragma unroll
+                        for (int i = 0; i < 4; i++)
+                            m4[i] = fmaxf(m4[i], c + 4 + i < TC_STEP ? fmaxf(x[c + i], x[c + 4 + i])
+                                                                     : x[c + i]);
+                    far = fmaf(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), rf, lvtop);
+                }
+                const bool need = far > M + TC_TOP;
+                // PV of this stream's step before has read P and is in O
+                if (!first) {
+                    if (!(ok = all(wait(Sh::B_PV + t, (n - 1) & 1)))) break;
+                    tc::fence_after_sync();
+                }
+                if (__any_sync(0xffffffffu, need)) {
+                    const float m = need ? far - TC_AIM : M;
+                    const float f = tr_ex2(M - m);
+                    M = m;
+                    sum = __fmul2_rn(sum, make_float2(f, f));
+                    if (!first) {
+#pragma unroll 1
+                        for (int c = 0; c < HD / 32; c++) {
+                            float o[32];
+                            tc::tmem_ld32(tO + 32 * c, o);
+#pragma unroll
+                            for (int i = 0; i < 32; i++) o[i] *= f;
+                            tc::tmem_st32(tO + 32 * c, o);
+                        }
+                    }
+                }
+                first = false;
+                const float* vs = km + 128;
+                const float2 rf2 = make_float2(rf, rf), nm = make_float2(-M, -M);
+#pragma unroll
+                for (int q = 0; q < 2; q++) {
+                    float hi[32], lo[32];  // 32 columns of fp16 pairs
+#pragma unroll
+                    for (int c = 0; c < 32; c += 2) {
+                        const int e = 64 * q + 2 * c;
+                        const float4 v4 = *reinterpret_cast<const float4*>(vs + e);
+                        const float2 vv[2] = {make_float2(v4.x, v4.y), make_float2(v4.z, v4.w)};
+#pragma unroll
+                        for (int k = 0; k < 2; k++) {
+                            const float2 y =
+                                __ffma2_rn(make_float2(x[e + 2 * k], x[e + 2 * k + 1]), rf2, nm);
+                            const float2 p = make_float2(tr_ex2(y.x), tr_ex2(y.y));
+                            sum = __fadd2_rn(sum, p);
+                            float2 wt = __fmul2_rn(p, vv[k]);
+                            if (masked) {  // a masked token's V step may be anything
+                                wt.x = p.x == 0.0f ? 0.0f : wt.x;
+                                wt.y = p.y == 0.0f ? 0.0f : wt.y;
+                            }
+                            const uint32_t h = f2_to_h2(wt.x, wt.y);
+                            hi[c + k] = __uint_as_float(h);
+                            if (HILO) {
+                                const float2 b = h2_to_f2(h);
+                                lo[c + k] = __uint_as_float(f2_to_h2(wt.x - b.x, wt.y - b.y));
+                            }
+                        }
+                    }
+                    tc::tmem_st32(tP + 32 * q, hi);
+                    if (HILO) tc::tmem_st32(tP + 64 + 32 * q, lo);
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) tc_arrive(bars + Sh::B_P + 2 * t + q);
+                }
+                n++;
+            }
+            if (!ok) break;
+            if (!first) {
+                if (!(ok = all(wait(Sh::B_PV + t, (n - 1) & 1)))) break;
+                tc::fence_after_sync();
+            }
+            // ---- the list's result.  The streams of one tile meet: each then writes half
+            // of the dimensions from both O's.
+            float den = sum.x + sum.y;
+            float f[2] = {1.0f, 0.0f};
+            if (SPLIT) {
+                ex[128 * t + row] = make_float2(M, den);
+                __syncwarp();
+                if (lane == 0) tc_arrive(bars + Sh::B_XF);
+                if (!(ok = all(wait(Sh::B_XF, xn & 1)))) break;
+                const float2 a = ex[row], b = ex[128 + row];
+                M = fmaxf(a.x, b.x);
+                f[0] = a.y == 0.0f ? 0.0f : tr_ex2(a.x - M);
+                f[1] = b.y == 0.0f ? 0.0f : tr_ex2(b.x - M);
+                den = a.y * f[0] + b.y * f[1];
+            }
+            // a share cuts at most its first and its last list
+            const size_t at = (((size_t)blockIdx.x * 2 + (piece == 0 ? 0 : 1)) * NR + 128 * tile + row);
+            const bool mine = row < rows;
+            const float inv = it.whole() ? (den == 0.0f ? 0.0f : __fdiv_rn(1.0f, den)) : 1.0f;
+            const size_t out = ((size_t)(it.s.q0 + node) * P.nq + (size_t)it.h * P.G +
+                                (r0 + row) % P.G) * HD;
+#pragma unroll 1
+            for (int c = SPLIT ? 2 * t : 0; c < (SPLIT ? 2 * t + 2 : 4); c++) {
+                float o[32];
+                tc::tmem_ld32((SPLIT ? col_o(0) + lanes : tO) + 32 * c, o);
+                if (SPLIT) {
+                    float o1[32];
+                    tc::tmem_ld32(col_o(1) + lanes + 32 * c, o1);
+#pragma unroll
+                    for (int i = 0; i < 32; i++)  // a stream without steps left nothing there
+                        o[i] = (f[0] == 0.0f ? 0.0f : o[i] * f[0]) + (f[1] == 0.0f ? 0.0f : o1[i] * f[1]);
+                } else if (den == 0.0f) {
+#pragma unroll
+                    for (int i = 0; i < 32; i++) o[i] = 0.0f;
+                }
+                if (mine) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+                        const float4 y = make_float4(o[i] * inv, o[i + 1] * inv, o[i + 2] * inv,
+                                                     o[i + 3] * inv);
+                        if (it.whole())
+                            store_out4(P.out, P.dtype, out + 32 * c + i, y);
+                        else
+                            *reinterpret_cast<float4*>(P.part_acc + at * HD + 32 * c + i) = y;
+                    }
+                }
+            }
+            if (mine && !it.whole() && (!SPLIT || t == 0)) P.part_ms[at] = make_float2(M, den);
+            tc::fence_before_sync();
+            if (SPLIT) {
+                // both O's and the exchange are read before either is written again
+                __syncwarp();
+                if (lane == 0) tc_arrive(bars + Sh::B_XE);
+                if (!(ok = all(wait(Sh::B_XE, xn & 1)))) break;
+            }
+            xn++;
+        }
+    }
+    __syncwarp();
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == 0) {
+        __syncwarp();
+        tc::fence_after_sync();
+        tc::tmem_dealloc(tbase, 512);
+    }
+}
+
+// The lists that shares have cut:
+//   m = max_c m_c, out = sum_c acc_c 2^(m_c - m) / sum_c S_c 2^(m_c - m).
+// Block (c, y) merges rows 8 y .. of the list that ends inside share c but began
+// before it, a warp per row.  A CTA's piece is its part 0 if it is the share's first,
+// else part 1.  After a CTA has given up (some parts are missing) every row stays as
+// it was; the mark goes with kq8_workspace_init, which a failed call asks for.
+constexpr int TM_WARPS = 8;
+__global__ void __launch_bounds__(TM_WARPS * 32)
+    kq8_tree_merge_kernel(const __grid_constant__ TreeParams P, const int NR) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, ctas = gridDim.x;
+    __shared__ TcShare share_sm;
+    if (warp == 0) {
+        const TcShare sh = tc_share(P, NR, blockIdx.x, ctas);
+        if (lane == 0) share_sm = sh;
+    }
+    __syncthreads();
+    const TcShare sh = share_sm;
+    TcWalk walk(P, sh);
+    TcItem it;
+    if (P.status[1] != 0u || !walk.next(P, NR, it)) return;
+    if (it.step0 == 0 || it.step0 + it.steps < it.s.steps) return;
+    const int row = blockIdx.y * TM_WARPS + warp, rr = it.rt * NR + row;
+    if (row >= NR || rr >= it.s.nb * P.G) return;
+    const int64_t first = sh.begin - it.step0;  // the list's first step
+    int c = (int)blockIdx.x;
+    float m = TC_M_INIT, den = 0.0f;
+    float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (;; c--) {
+        const int64_t begin = tc_bound(sh.total, c, ctas);
+        const int64_t end = tc_bound(sh.total, c + 1, ctas);
+        if (begin < end) {  // a share of nothing wrote nothing
+            const size_t at = ((size_t)c * 2 + (begin < first ? 1 : 0)) * NR + row;
+            const float2 ms = P.part_ms[at];
+            const float4 x = reinterpret_cast<const float4*>(P.part_acc + at * HD)[lane];
+            const float mn = fmaxf(m, ms.x);
+            const float fo = tr_ex2(m - mn), fn = tr_ex2(ms.x - mn);
+            den = den * fo + ms.y * fn;
+            a.x = a.x * fo + x.x * fn;
+            a.y = a.y * fo + x.y * fn;
+            a.z = a.z * fo + x.z * fn;
+            a.w = a.w * fo + x.w * fn;
+            m = mn;
+        }
+        if (begin <= first) break;
+    }
+    const float inv = den == 0.0f ? 0.0f : 1.0f, dv = den == 0.0f ? 1.0f : den;
+    store_out4(P.out, P.dtype,
+               ((size_t)(it.s.q0 + rr / P.G) * P.nq + (size_t)it.h * P.G + rr % P.G) * HD + 4 * lane,
+               make_float4(a.x / dv * inv, a.y / dv * inv, a.z / dv * inv, a.w / dv * inv));
+}
+
+template <int T, bool HILO>
+int launch_tc(const TreeParams& p, int ctas, cudaStream_t s) {
+    static std::atomic<uint64_t> opted{0};
+    return launch_smem(kq8_tree_tc_kernel<T, HILO>, opted, dim3((unsigned)ctas), TC_THREADS,
+                       TcShape<T, HILO>::SMEM, s, p);
+}
+
+}  // namespace
+
+int launch_tree_tc(const TreeParams& p, int tile_rows, int ctas, cudaStream_t s) {
+    int rc = p.dtype != KQ8_BF16 ? launch_tc<1, true>(p, ctas, s)
+             : tile_rows == 128  ? launch_tc<1, false>(p, ctas, s)
+                                 : launch_tc<2, false>(p, ctas, s);
+    if (rc || ctas == 1) return rc;
+    return launch_pdl(kq8_tree_merge_kernel, dim3((unsigned)ctas, (unsigned)(tile_rows / TM_WARPS)),
+                      TM_WARPS * 32, s, p, tile_rows);
+}
+
+}  // namespace kq8
