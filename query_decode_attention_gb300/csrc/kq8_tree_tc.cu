@@ -5,9 +5,13 @@
 // Each row is computed as in kq8_tree.cu, up to 128 rows to a tile (MMA M, TMEM lanes):
 //   S [128 rows x 128 tokens] = Q K^T      O [128 rows x 128 dims] += P V.
 // Q's rows are the method's codes times their block scales, as fp16 with a power of two
-// per row that puts the row's largest near 2^13; K's and V's codes are exact in fp16;
-// the weights p * vstep enter as fp16.  bf16 outputs (whose own rounding is 2^-9) take Q
-// and P at 11 bits, the others as hi and lo parts (22 bits), each an MMA of its own.
+// per row that puts the row's largest near 2^13.  Outputs of 24 and 11 bits take K's and
+// V's codes as they are (exact in fp16), the tokens' scales in fp32 beside the softmax,
+// and Q and the weights p * vstep as fp16 hi and lo parts (22 bits), each an MMA of its
+// own.  bf16 outputs, whose own rounding is 2^-9, take Q and P at 11 bits, and K and V
+// already multiplied by their token's scale (relative to a power of two per 32 tokens),
+// 11 bits too: that leaves the softmax one multiply-add and one exponential per score
+// instead of two loads and three operations (a step of one tile 5500 -> @@ cycles).
 //
 // What bounds it.  Per 128-token step shared memory carries the raw bytes in and out of
 // the ring (66 KB), the widened operands in (64 KB) and, per tile, Q and K (64 KB) and V
@@ -44,10 +48,10 @@ namespace kq8 {
 namespace {
 
 constexpr int TC_STEP = 128;                     // tokens per step
-constexpr int TC_THREADS = 16 * 32;
-constexpr int TC_W_WIDEN = 8, TC_W_S = 12, TC_W_PV = 13, TC_W_LOAD = 15;
-// registers per thread, 128 at launch: 2 * 184 + 80 + 64 = 4 * 128
-constexpr int TC_REGS_SOFTMAX = 184, TC_REGS_WIDEN = 80, TC_REGS_REST = 64;
+constexpr int TC_THREADS = 20 * 32;
+constexpr int TC_W_WIDEN = 8, TC_W_S = 16, TC_W_PV = 17, TC_W_LOAD = 19;
+// registers per thread, 96 at launch: 2 * 136 + 2 * 64 + 80 = 5 * 96
+constexpr int TC_REGS_SOFTMAX = 136, TC_REGS_WIDEN = 64, TC_REGS_REST = 80;
 constexpr uint32_t TC_PANEL = TC_STEP * 128;     // 128 rows x 64 fp16
 constexpr uint32_t TC_OP = 2 * TC_PANEL;         // an operand: 128 rows x 128 fp16
 constexpr float TC_M_INIT = -1e30f;              // reference of a row that saw nothing
@@ -60,14 +64,16 @@ struct TcShape {
     static constexpr int NS = HILO ? 1 : 2;            // streams
     // Rings, as far as shared memory goes.  A parity wait is only sound for a waiter
     // that waits for every phase of a barrier, in order: so the raw ring is a multiple
-    // of the four widening warps long (a place has one consumer), and with one tile and
-    // two streams V has two places, one per stream (stream = step % 2).
+    // of four long (a place has the same two consumers, sub-tile w's K and V warp), and
+    // with one tile and two streams V has two places, one per stream (stream = step % 2).
     static constexpr int RAWN = 8, VB = T == 1 && !HILO ? 2 : 1;
     static constexpr uint32_t Q = 0, K = (T + (HILO ? 1 : 0)) * TC_OP, V = K + TC_OP,
                               RAW = V + VB * TC_OP,
                               SC = RAW + RAWN * STAGE_BYTES,  // [4][3][128] floats
-                              META = SC + 4 * 3 * 512,        // [4][4] (missing, largest log2 V step)
-                              RF = META + 4 * 4 * 8,          // [T][128] row factors
+                              // [4][4]: something is missing or not finite, a bound of log2
+                              // of the V steps, K's factor, V's exponent
+                              META = SC + 4 * 3 * 512,
+                              RF = META + 4 * 4 * 16,         // [T][128] row factors
                               EX = RF + T * 512,              // [2][128] (m, sum)
                               MISC = EX + 2048,               // TMEM, abort, flags, share
                               BAR = MISC + 128, SMEM = BAR + 512 + 1024;
@@ -75,7 +81,7 @@ struct TcShape {
     static constexpr int B_RAWF = 0, B_RAWE = B_RAWF + RAWN, B_KF = B_RAWE + RAWN, B_KE = B_KF + 1,
                          B_VF = B_KE + 1, B_VE = B_VF + VB, B_SCF = B_VE + VB,
                          B_SF = B_SCF + 4,   // [stream], hi and lo: [S buffer]
-                         B_SR = B_SF + 2,    // S is in registers: [0], hi and lo: [S buffer]
+                         B_SR = B_SF + 2,    // hi and lo: S has been read, [S buffer]
                          B_P = B_SR + 2,     // [stream][half]
                          B_PV = B_P + 4,     // [stream]
                          B_QF = B_PV + 2, B_XF = B_QF + 1, B_XE = B_XF + 1,
@@ -85,14 +91,20 @@ struct TcShape {
 
 __device__ __forceinline__ int tc_rho(int r) { return (r & ~6) | ((r & 2) << 1) | ((r & 4) >> 1); }
 
-// 8 int8 codes -> 8 fp16, exactly.
-__device__ __forceinline__ uint4 widen8(uint32_t a, uint32_t b) {
+// 8 int8 codes -> 8 fp16: exactly, or times an fp16 pair of equals.
+template <bool EXACT>
+__device__ __forceinline__ uint4 widen8(uint32_t a, uint32_t b, uint32_t f) {
     const uint32_t u = a ^ 0x80808080u, v = b ^ 0x80808080u;
-    return make_uint4(hsub2(__byte_perm(u, 0x64646464u, 0x4140), 0x64806480u),
-                      hsub2(__byte_perm(u, 0x64646464u, 0x4342), 0x64806480u),
-                      hsub2(__byte_perm(v, 0x64646464u, 0x4140), 0x64806480u),
-                      hsub2(__byte_perm(v, 0x64646464u, 0x4342), 0x64806480u));
+    auto half = [&](uint32_t w, uint32_t sel) {
+        const uint32_t x = hsub2(__byte_perm(w, 0x64646464u, sel), 0x64806480u);
+        if (EXACT) return x;
+        uint32_t r;
+        asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(f));
+        return r;
+    };
+    return make_uint4(half(u, 0x4140), half(u, 0x4342), half(v, 0x4140), half(v, 0x4342));
 }
+__device__ __forceinline__ uint32_t make_half2_bits(float x) { return f2_to_h2(x, x); }
 __device__ __forceinline__ void tc_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
@@ -218,6 +230,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     if (tid == 0) {
         for (int i = 0; i < Sh::B_COUNT; i++) {
             uint32_t cnt = 1;
+            if (i >= Sh::B_RAWE && i < Sh::B_KF) cnt = 2;
             if (i == Sh::B_KF || (i >= Sh::B_VF && i < Sh::B_VE)) cnt = 4;
             if (i >= Sh::B_VE && i < Sh::B_SCF) cnt = T;  // a PV thread per tile
             if (i >= Sh::B_SCF && i < Sh::B_SF) cnt = 4;
@@ -263,12 +276,12 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     };
     auto all = [](bool x) { return __all_sync(0xffffffffu, x) != 0; };
     float* sc = reinterpret_cast<float*>(sm + Sh::SC);
-    float2* meta = reinterpret_cast<float2*>(sm + Sh::META);
+    float4* meta = reinterpret_cast<float4*>(sm + Sh::META);
     float* rf_sm = reinterpret_cast<float*>(sm + Sh::RF);
     // TMEM columns
     auto col_o = [&](int t) { return tbase + 128 * t; };
-    auto col_s = [&](uint32_t n) { return tbase + (HILO ? 128 + 128 * (n & 1) : 256); };
-    auto col_p = [&](int t) { return tbase + 384 + 64 * t; };  // hi and lo: 384, 448
+    auto col_s = [&](int t, uint32_t n) { return tbase + (HILO ? 128 + 128 * (n & 1) : 256 + 128 * t); };
+    auto col_p = [&](int t) { return tbase + (HILO ? 384 : 256 + 128 * t); };  // lo: 64 on
 
     if (warp >= TC_W_S) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(TC_REGS_REST));
@@ -337,30 +350,35 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             const uint64_t dq = tc::sdesc_sw128(smem_u32(sm + Sh::Q), 16, 1024);
             const uint64_t dk = tc::sdesc_sw128(smem_u32(sm + Sh::K), 16, 1024);
             constexpr uint32_t IDS = tc::IDesc<128, TC_STEP, false>::value;
-            uint32_t g = 0, n = 0, qn = 0;  // steps, products, lists so far
+            uint32_t g = 0, qn = 0;    // steps, lists so far
+            uint32_t n[2] = {0u, 0u};  // products of each stream so far
             bool ok = true;
             while (ok && walk.next(P, NR, it)) {
                 ok = wait(Sh::B_QF, qn++ & 1);
                 for (int j = 0; ok && j < it.steps; j++, g++) {
                     if (!(ok = wait(Sh::B_KF, g & 1))) break;
-                    for (int t = 0; ok && t < T; t++, n++) {
-                        // the scores there before are in registers
+                    for (int i = 0; ok && i < T; i++) {
+                        const int t = SPLIT ? (int)(g & 1) : i;
+                        // the place is free: hi and lo, when the scores have been read, else
+                        // when PV has read the weights over them
                         if (HILO) {
-                            if (n >= 2 && !(ok = wait(Sh::B_SR + (n & 1), ((n - 2) >> 1) & 1))) break;
-                        } else if (n >= 1 && !(ok = wait(Sh::B_SR, (n - 1) & 1))) {
+                            if (n[0] >= 2 && !(ok = wait(Sh::B_SR + (n[0] & 1), ((n[0] - 2) >> 1) & 1)))
+                                break;
+                        } else if (n[t] >= 1 && !(ok = wait(Sh::B_PV + t, (n[t] - 1) & 1))) {
                             break;
                         }
                         tc::fence_after_sync();
 #pragma unroll
                         for (int part = 0; part < (HILO ? 2 : 1); part++) {
-                            const uint64_t a = dq + (uint64_t)((t + part) * (TC_OP >> 4));
+                            const uint64_t a = dq + (uint64_t)((i + part) * (TC_OP >> 4));
 #pragma unroll
                             for (int kk = 0; kk < HD / 16; kk++) {
                                 const uint64_t o = (kk >> 2) * (TC_PANEL >> 4) + (kk & 3) * 2;
-                                tc::mma_f16(col_s(n), a + o, dk + o, IDS, kk > 0 || part > 0);
+                                tc::mma_f16(col_s(t, n[0]), a + o, dk + o, IDS, kk > 0 || part > 0);
                             }
                         }
-                        tc::mma_commit(bars + Sh::B_SF + (HILO ? n & 1 : SPLIT ? g & 1 : t));
+                        tc::mma_commit(bars + Sh::B_SF + (HILO ? n[0] & 1 : t));
+                        n[t]++;
                     }
                     if (ok) tc::mma_commit(bars + Sh::B_KE);
                 }
@@ -391,7 +409,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                         for (int kk = 4 * half; kk < 4 * half + 4; kk++) {
                             const uint64_t b = v + (uint64_t)(kk * (2048 >> 4));
                             tc::mma_f16_ta(col_o(t), col_p(t) + 8 * kk, b, IDO, !first || kk > 0);
-                            if (HILO) tc::mma_f16_ta(col_o(t), col_p(1) + 8 * kk, b, IDO, true);
+                            if (HILO) tc::mma_f16_ta(col_o(t), col_p(t) + 64 + 8 * kk, b, IDO, true);
                         }
                     }
                     if (!ok) break;
@@ -407,89 +425,112 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         }
     } else if (warp >= TC_W_WIDEN) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(TC_REGS_WIDEN));
-        const int w = warp - TC_W_WIDEN;  // sub-tile of a step
+        const int w = (warp - TC_W_WIDEN) & 3;  // sub-tile of a step
+        const bool is_v = warp >= TC_W_WIDEN + 4;
         const float kmul = inv127() * P.scale * TR_LOG2E;
+        // a power of two above x (finite, >= 0)
+        auto above = [](float x) { return min(max((int)(__float_as_uint(x) >> 23) - 126, -90), 100); };
         uint32_t g = 0;
         bool ok = true;
         while (ok && walk.next(P, NR, it)) {
             for (int j = 0; j < it.steps; j++, g++) {
                 const uint32_t ri = 4 * g + w;
-                const int s = ri % RAWN;
+                const int s = ri % RAWN, place = VB == 2 ? g & 1 : 0;
                 if (!(ok = all(wait(Sh::B_RAWF + s, (ri / RAWN) & 1)))) break;
                 const uint8_t* st = sm + Sh::RAW + s * STAGE_BYTES;
-                uint4 x[8];
-                {
+                // lane = operand row: its token's K multiplier or V step
+                const int tok = krow(tc_rho(lane));
+                const float* rs = reinterpret_cast<const float*>(st + SUB_K_BYTES + SUB_V_BYTES);
+                const bool have = sub_ok[s] != 0;
+                const bool live = have && (4 * (it.step0 + j) + w) * TILE + tok < it.s.n;
+                // a token past the end or on a missing page counts for nothing
+                const float km = live ? __fmul_rn(rs[tok], kmul) : 0.0f;
+                const float vstep = live ? __fmul_rn(rs[32 + tok], inv127()) : 0.0f;
+                const uint32_t vb = __float_as_uint(fabsf(vstep)) < 0x7F800000u
+                                        ? __float_as_uint(fabsf(vstep)) : 0u;
+                const int ve = above(__uint_as_float(__reduce_max_sync(0xffffffffu, vb)));
+                if (!is_v) {
+                    const uint32_t kb = __float_as_uint(fabsf(km)) < 0x7F800000u
+                                            ? __float_as_uint(fabsf(km)) : 0u;
+                    const int ke = above(__uint_as_float(__reduce_max_sync(0xffffffffu, kb)));
+                    const bool odd = !have || __any_sync(0xffffffffu, !(fabsf(vstep) < INFINITY));
+                    if (g > 0 && !(ok = all(wait(Sh::B_KE, (g - 1) & 1)))) break;
+                    // (The place of the step's scales was last read for step g - 4.  S(g - 1),
+                    // which freed K's place, went over scores whose weights PV had read: of
+                    // step g - 3 or g - 2, one stream's, and the other's step came before.)
+                    float* d = sc + (g & 3) * 384 + 32 * w + lane;
+                    d[0] = km;
+                    d[128] = vstep;
+                    float lv;  // log2 of the V step, from below
+                    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(lv) : "f"(vstep));
+                    lv = lv < 128.0f ? fmaxf(lv, -90.0f) : INFINITY;  // not finite: the row is lost
+                    d[256] = have ? lv : -INFINITY;                   // a missing page's: masked
+                    if (lane == 0)
+                        meta[(g & 3) * 4 + w] = make_float4(odd ? 1.0f : 0.0f, (float)ve,
+                                                            HILO ? 1.0f : pow2i(ke), 0.0f);
                     // K: lane = (position pair, 16-byte half); its 16 codes are chunks c, c + 1
                     // of the row's panel
-#pragma unroll
-                    for (int i = 0; i < 8; i++)
-                        x[i] = *reinterpret_cast<const uint4*>(st + 512 * i + 16 * lane);
-                    const int t = krow(tc_rho(lane));
-                    const float* rs = reinterpret_cast<const float*>(st + SUB_K_BYTES + SUB_V_BYTES);
-                    const bool have = sub_ok[s] != 0;
-                    const bool live = have && (4 * (it.step0 + j) + w) * TILE + t < it.s.n;
-                    const float ks = rs[t], vs = rs[32 + t];
-                    if (g > 0 && !(ok = all(wait(Sh::B_KE, (g - 1) & 1)))) break;
-                    // a token past the end or on a missing page counts for nothing.  (The
-                    // multipliers' place was last read for step g - 4.  S(g - 1), which freed
-                    // K's place, was issued when the scores before it had been read, by
-                    // streams that had therefore begun step g - 3 or a later one of theirs.)
-                    float* d = sc + (g & 3) * 384 + 32 * w + lane;
-                    const float vstep = live ? __fmul_rn(vs, inv127()) : 0.0f;
-                    float lv;  // log2 of the V step, from below; what is not finite does not count
-                    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(lv) : "f"(vstep));
-                    lv = lv < 128.0f ? fmaxf(lv, -90.0f) : -90.0f;
-                    d[0] = live ? __fmul_rn(ks, kmul) : 0.0f;
-                    d[128] = vstep;
-                    d[256] = lv;
-                    const float top = warp_max(lv);
-                    if (lane == 0) meta[(g & 3) * 4 + w] = make_float2(have ? 0.0f : 1.0f, top);
-                    uint8_t* dst = sm + Sh::K;
-#pragma unroll
-                    for (int i = 0; i < 8; i++) {
-                        const int blk = i >> 1, row = 32 * w + tc_rho((i & 1) * 16 + (lane >> 1));
+                    const uint32_t f = make_half2_bits(km * pow2i(-ke));
+                    const int rowa = 32 * w + tc_rho(lane >> 1), x7 = rowa & 7;
+                    const uint32_t fa = __shfl_sync(0xffffffffu, f, rowa & 31);
+                    const uint32_t fb = __shfl_sync(0xffffffffu, f, (rowa + 16) & 31);
+                    uint4 xa = *reinterpret_cast<const uint4*>(st + 16 * lane);
+                    uint4 xb = *reinterpret_cast<const uint4*>(st + 512 + 16 * lane);
+#pragma unroll 1
+                    for (int blk = 0; blk < 4; blk++) {
+                        const uint4 ya = xa, yb = xb;
+                        if (blk < 3) {
+                            xa = *reinterpret_cast<const uint4*>(st + 1024 * (blk + 1) + 16 * lane);
+                            xb = *reinterpret_cast<const uint4*>(st + 1024 * (blk + 1) + 512 + 16 * lane);
+                        }
                         const int c = (blk & 1) * 4 + (lane & 1) * 2;
-                        uint8_t* o = dst + (blk >> 1) * TC_PANEL + row * 128;
-                        *reinterpret_cast<uint4*>(o + ((c ^ (row & 7)) << 4)) =
-                            widen8(x[i].x, x[i].y);
-                        *reinterpret_cast<uint4*>(o + (((c + 1) ^ (row & 7)) << 4)) =
-                            widen8(x[i].z, x[i].w);
+                        uint8_t* o = sm + Sh::K + (blk >> 1) * TC_PANEL + rowa * 128;
+                        const int c0 = (c ^ x7) << 4, c1 = ((c + 1) ^ x7) << 4;
+                        *reinterpret_cast<uint4*>(o + c0) = widen8<HILO>(ya.x, ya.y, fa);
+                        *reinterpret_cast<uint4*>(o + c1) = widen8<HILO>(ya.z, ya.w, fa);
+                        *reinterpret_cast<uint4*>(o + 2048 + c0) = widen8<HILO>(yb.x, yb.y, fb);
+                        *reinterpret_cast<uint4*>(o + 2048 + c1) = widen8<HILO>(yb.z, yb.w, fb);
                     }
-                    tc::fence_smem_to_async();
-                    __syncwarp();
-                    if (lane == 0) {
-                        tc_arrive(bars + Sh::B_SCF + (g & 3));
-                        tc_arrive(bars + Sh::B_KF);
+                } else {
+                    if (g >= (uint32_t)VB && !(ok = all(wait(Sh::B_VE + place, (g / VB - 1) & 1)))) break;
+                    // V: tokens t and t + 4 (neighbouring positions), one panel each; a step that
+                    // is not finite counts as 0 here (the softmax sees to the rows that see it)
+                    const uint32_t f =
+                        make_half2_bits(fabsf(vstep) < INFINITY ? vstep * pow2i(-ve) : 0.0f);
+                    const int a = (lane >> 2) & 1, q = lane & 3, p = a ^ ((lane >> 3) & 1);
+                    const int u = (lane >> 4) + 4 * a;  // tokens 8 i + u and + 2
+                    const uint8_t* src = st + SUB_K_BYTES + u * HD + 64 * p + 16 * q;
+                    uint8_t* dst = sm + Sh::V + place * TC_OP + p * TC_PANEL + 32 * w * 128;
+                    uint4 xa = *reinterpret_cast<const uint4*>(src);
+                    uint4 xb = *reinterpret_cast<const uint4*>(src + 2 * HD);
+#pragma unroll 1
+                    for (int i = 0; i < 4; i++) {
+                        const uint4 ya = xa, yb = xb;
+                        if (i < 3) {
+                            xa = *reinterpret_cast<const uint4*>(src + (8 * i + 8) * HD);
+                            xb = *reinterpret_cast<const uint4*>(src + (8 * i + 10) * HD);
+                        }
+                        const int ra = tc_rho(kpos(8 * i + u)), rb = tc_rho(kpos(8 * i + u + 2));
+                        const uint32_t fa = __shfl_sync(0xffffffffu, f, ra);
+                        const uint32_t fb = __shfl_sync(0xffffffffu, f, rb);
+                        uint8_t *oa = dst + ra * 128, *ob = dst + rb * 128;
+                        *reinterpret_cast<uint4*>(oa + (((2 * q) ^ (ra & 7)) << 4)) =
+                            widen8<HILO>(ya.x, ya.y, fa);
+                        *reinterpret_cast<uint4*>(oa + (((2 * q + 1) ^ (ra & 7)) << 4)) =
+                            widen8<HILO>(ya.z, ya.w, fa);
+                        *reinterpret_cast<uint4*>(ob + (((2 * q) ^ (rb & 7)) << 4)) =
+                            widen8<HILO>(yb.x, yb.y, fb);
+                        *reinterpret_cast<uint4*>(ob + (((2 * q + 1) ^ (rb & 7)) << 4)) =
+                            widen8<HILO>(yb.z, yb.w, fb);
                     }
-                }
-                // V: tokens t and t + 4 (neighbouring positions), one panel each
-                const int a = (lane >> 2) & 1, q = lane & 3, p = a ^ ((lane >> 3) & 1);
-#pragma unroll
-                for (int i = 0; i < 8; i++) {
-                    const int pi = 2 * i + (lane >> 4);
-                    const int t = (pi >> 2) * 8 + (pi & 3) + 4 * a;
-                    x[i] = *reinterpret_cast<const uint4*>(st + SUB_K_BYTES + t * HD + 64 * p + 16 * q);
-                }
-                // the raw place is given back as soon as its bytes are in registers
-                __syncwarp();
-                if (lane == 0) tc_arrive(bars + Sh::B_RAWE + s);
-                const int place = VB == 2 ? g & 1 : 0;
-                if (g >= (uint32_t)VB && !(ok = all(wait(Sh::B_VE + place, (g / VB - 1) & 1)))) break;
-                uint8_t* dst = sm + Sh::V + place * TC_OP;
-#pragma unroll
-                for (int i = 0; i < 8; i++) {
-                    const int pi = 2 * i + (lane >> 4);
-                    const int t = (pi >> 2) * 8 + (pi & 3) + 4 * a;
-                    const int row = 32 * w + tc_rho(kpos(t));
-                    uint8_t* o = dst + p * TC_PANEL + row * 128;
-                    *reinterpret_cast<uint4*>(o + (((2 * q) ^ (row & 7)) << 4)) =
-                        widen8(x[i].x, x[i].y);
-                    *reinterpret_cast<uint4*>(o + (((2 * q + 1) ^ (row & 7)) << 4)) =
-                        widen8(x[i].z, x[i].w);
                 }
                 tc::fence_smem_to_async();
                 __syncwarp();
-                if (lane == 0) tc_arrive(bars + Sh::B_VF + place);
+                if (lane == 0) {
+                    tc_arrive(bars + Sh::B_RAWE + s);
+                    if (!is_v) tc_arrive(bars + Sh::B_SCF + (g & 3));
+                    tc_arrive(bars + (is_v ? Sh::B_VF + place : Sh::B_KF));
+                }
             }
         }
     } else {
@@ -546,7 +587,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             const float rf = rf_sm[128 * tile + row];
             const int node = (r0 + row) / P.G;
             float M = TC_M_INIT;
-            float2 sum = make_float2(0.0f, 0.0f);
+            float sum = 0.0f;
             bool first = true;
             for (int j = 0; ok && j < it.steps; j++, g++) {
                 if (SPLIT && (int)(g & 1) != t) continue;
@@ -556,63 +597,63 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                 ok = ok && all(wait(Sh::B_SF + (HILO ? n & 1 : t), sn & 1));
                 if (!ok) break;
                 tc::fence_after_sync();
-                float x[TC_STEP];
-                tc::tmem_ld_cols<TC_STEP>(col_s(n) + lanes, x);
-                tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0) tc_arrive(bars + Sh::B_SR + (HILO ? n & 1 : 0));
-                // scores (base 2) over the row's factor
-#pragma unroll
-                for (int c = 0; c < TC_STEP; c += 4) {
-                    const float4 k4 = *reinterpret_cast<const float4*>(km + c);
-                    const float2 a = __fmul2_rn(make_float2(x[c], x[c + 1]), make_float2(k4.x, k4.y));
-                    const float2 b =
-                        __fmul2_rn(make_float2(x[c + 2], x[c + 3]), make_float2(k4.z, k4.w));
-                    x[c] = a.x;
-                    x[c + 1] = a.y;
-                    x[c + 2] = b.x;
-                    x[c + 3] = b.y;
-                }
                 const int tile0 = 4 * (it.step0 + j);  // the step's first sub-tile
-                float2 mt[4];
-                bool gone = false;
-                float lvtop = -90.0f;
+                const float4* mt = meta + (g & 3) * 4;
+                const bool masked = (tile0 + 4) * TILE > it.s.base || mt[0].x + mt[1].x + mt[2].x + mt[3].x != 0.0f;
+                const uint32_t tS = col_s(t, n) + lanes;
+                bool lost = false;  // the row sees a V step that is not finite
+                // columns 32 w .. + 31: x * f is the score (base 2), -inf where the row does not
+                // see the token; top bounds the exponents of the V steps that it sees
+                auto fetch = [&](int w, float (&x)[32], float& f, float& top) {
+                    tc::tmem_ld32(tS + 32 * w, x);
+                    const float4 m = mt[w];
+                    f = rf * m.z;
+                    top = m.y;
+                    if (HILO) {
 #pragma unroll
-                for (int w = 0; w < 4; w++) {
-                    mt[w] = meta[(g & 3) * 4 + w];
-                    gone |= mt[w].x != 0.0f;
-                    lvtop = fmaxf(lvtop, mt[w].y);
-                }
-                const bool masked = (tile0 + 4) * TILE > it.s.base || gone;
-                float far;  // a bound of the row's weights' exponents
-                if (masked) {
-                    // what the row sees, 32 tokens to a word
-                    far = -INFINITY;
-                    const float* lv = km + 256;
-#pragma unroll
-                    for (int w = 0; w < 4; w++) {
-                        uint32_t win = 0u;
-                        if (row < rows && mt[w].x == 0.0f)
-                            win = node_window(P, it.s.q0, node, it.s.nb, (tile0 + w) * TILE - it.s.base);
-#pragma unroll
-                        for (int c = 0; c < 32; c++) {
-                            const bool on = (win >> krow(tc_rho(c))) & 1u;
-                            x[32 * w + c] = on ? x[32 * w + c] : -INFINITY;
-                            far = fmaxf(far, fmaf(x[32 * w + c], rf, lv[32 * w + c]));
+                        for (int c = 0; c < 32; c += 4) {
+                            const float4 k4 = *reinterpret_cast<const float4*>(km + 32 * w + c);
+                            const float2 a =
+                                __fmul2_rn(make_float2(x[c], x[c + 1]), make_float2(k4.x, k4.y));
+                            const float2 b =
+                                __fmul2_rn(make_float2(x[c + 2], x[c + 3]), make_float2(k4.z, k4.w));
+                            x[c] = a.x;
+                            x[c + 1] = a.y;
+                            x[c + 2] = b.x;
+                            x[c + 3] = b.y;
                         }
                     }
-                } else {
+                    if (masked) {
+                        uint32_t win = 0u;
+                        if (row < rows)
+                            win = node_window(P, it.s.q0, node, it.s.nb, (tile0 + w) * TILE - it.s.base);
+                        float most = -90.0f;
+#pragma unroll
+                        for (int c = 0; c < 32; c++) {
+                            const float l = km[256 + 32 * w + c];
+                            const bool on = ((win >> krow(tc_rho(c))) & 1u) && l > -INFINITY;
+                            lost |= on && l == INFINITY;
+                            if (on && l < INFINITY) most = fmaxf(most, l);
+                            x[c] = on ? x[c] : -INFINITY;
+                        }
+                        if (HILO) top = most + 1.0f;
+                    }
+                };
+                float far = -INFINITY;  // a bound of the row's weights' exponents
+#pragma unroll 1
+                for (int w = 0; w < 4; w++) {
+                    float x[32], f, top;
+                    fetch(w, x, f, top);
                     float m4[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-                    for (int c = 4; c < TC_STEP; c += 8)
+                    for (int c = 4; c < 32; c += 8)
 #pragma unroll
                         for (int i = 0; i < 4; i++)
-                            m4[i] = fmaxf(m4[i], c + 4 + i < TC_STEP ? fmaxf(x[c + i], x[c + 4 + i])
-                                                                     : x[c + i]);
-                    far = fmaf(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), rf, lvtop);
+                            m4[i] = fmaxf(m4[i], c + 4 + i < 32 ? fmaxf(x[c + i], x[c + 4 + i]) : x[c + i]);
+                    far = fmaxf(far, fmaf(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), f, top));
                 }
                 const bool need = far > M + TC_TOP;
-                // PV of this stream's step before has read P and is in O
+                // PV of this stream's step before is in O (and, hi and lo, has read P)
                 if (!first) {
                     if (!(ok = all(wait(Sh::B_PV + t, (n - 1) & 1)))) break;
                     tc::fence_after_sync();
@@ -621,7 +662,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                     const float m = need ? far - TC_AIM : M;
                     const float f = tr_ex2(M - m);
                     M = m;
-                    sum = __fmul2_rn(sum, make_float2(f, f));
+                    sum *= f;
                     if (!first) {
 #pragma unroll 1
                         for (int c = 0; c < HD / 32; c++) {
@@ -634,41 +675,48 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                     }
                 }
                 first = false;
-                const float* vs = km + 128;
-                const float2 rf2 = make_float2(rf, rf), nm = make_float2(-M, -M);
+#pragma unroll 1
+                for (int w = 0; w < 4; w++) {
+                    float x[32], f, top;
+                    fetch(w, x, f, top);
+                    // bf16: p * 2^(the sub-tile's V exponent) is the weight itself
+                    const float ve = HILO ? 0.0f : mt[w].y;
+                    const float2 f2 = make_float2(f, f), o2 = make_float2(ve - M, ve - M);
+                    float2 s2 = make_float2(0.0f, 0.0f);
+                    float hi[16], lo[16];  // 16 columns of fp16 pairs
 #pragma unroll
-                for (int q = 0; q < 2; q++) {
-                    float hi[32], lo[32];  // 32 columns of fp16 pairs
-#pragma unroll
-                    for (int c = 0; c < 32; c += 2) {
-                        const int e = 64 * q + 2 * c;
-                        const float4 v4 = *reinterpret_cast<const float4*>(vs + e);
-                        const float2 vv[2] = {make_float2(v4.x, v4.y), make_float2(v4.z, v4.w)};
-#pragma unroll
-                        for (int k = 0; k < 2; k++) {
-                            const float2 y =
-                                __ffma2_rn(make_float2(x[e + 2 * k], x[e + 2 * k + 1]), rf2, nm);
-                            const float2 p = make_float2(tr_ex2(y.x), tr_ex2(y.y));
-                            sum = __fadd2_rn(sum, p);
-                            float2 wt = __fmul2_rn(p, vv[k]);
+                    for (int i = 0; i < 16; i++) {
+                        const float2 y = __ffma2_rn(make_float2(x[2 * i], x[2 * i + 1]), f2, o2);
+                        const float2 p = make_float2(tr_ex2(y.x), tr_ex2(y.y));
+                        s2 = __fadd2_rn(s2, p);
+                        float2 wt = p;
+                        if (HILO) {
+                            wt = __fmul2_rn(p, *reinterpret_cast<const float2*>(km + 128 + 32 * w + 2 * i));
                             if (masked) {  // a masked token's V step may be anything
                                 wt.x = p.x == 0.0f ? 0.0f : wt.x;
                                 wt.y = p.y == 0.0f ? 0.0f : wt.y;
                             }
-                            const uint32_t h = f2_to_h2(wt.x, wt.y);
-                            hi[c + k] = __uint_as_float(h);
-                            if (HILO) {
-                                const float2 b = h2_to_f2(h);
-                                lo[c + k] = __uint_as_float(f2_to_h2(wt.x - b.x, wt.y - b.y));
-                            }
+                        }
+                        const uint32_t h = f2_to_h2(wt.x, wt.y);
+                        hi[i] = __uint_as_float(h);
+                        if (HILO) {
+                            const float2 b = h2_to_f2(h);
+                            lo[i] = __uint_as_float(f2_to_h2(wt.x - b.x, wt.y - b.y));
                         }
                     }
-                    tc::tmem_st32(tP + 32 * q, hi);
-                    if (HILO) tc::tmem_st32(tP + 64 + 32 * q, lo);
-                    tc::fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) tc_arrive(bars + Sh::B_P + 2 * t + q);
+                    sum = fmaf(s2.x + s2.y, pow2i(-(int)ve), sum);
+                    tc::tmem_st16(tP + 16 * w, hi);
+                    if (HILO) tc::tmem_st16(tP + 64 + 16 * w, lo);
+                    if (w & 1) {  // half of the weights, of which the product may begin
+                        tc::fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (HILO && w == 3) tc_arrive(bars + Sh::B_SR + (n & 1));
+                            tc_arrive(bars + Sh::B_P + 2 * t + (w >> 1));
+                        }
+                    }
                 }
+                if (lost) sum = NAN;
                 n++;
             }
             if (!ok) break;
@@ -678,7 +726,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             }
             // ---- the list's result.  The streams of one tile meet: each then writes half
             // of the dimensions from both O's.
-            float den = sum.x + sum.y;
+            float den = sum;
             float f[2] = {1.0f, 0.0f};
             if (SPLIT) {
                 ex[128 * t + row] = make_float2(M, den);
