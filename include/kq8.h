@@ -406,7 +406,8 @@ int kq8_decode_attn_q4(float* out, const float* q, const kq8_cache_t* cache,
  *                  (q4: 1/7) as one fp32 product, rounded once to dtype.  The rows
  *                  stored must not overlap (KQ8_ERR_INVALID_ARG).
  *   dtype  : KQ8_F32, KQ8_F16 or KQ8_BF16, of k and v both; pointers aligned to
- *            an element (16-byte aligned rows are copied 16 bytes at a time).
+ *            an element (rows whose base and strides are multiples of 8
+ *            elements are copied 8 elements at a time).
  *   slot, status : as kq8_append_kv.  A token with a negative or bad slot is
  *            skipped: its row of the cache (write) or of k and v (read) stays as
  *            it was.  A write's slots must be distinct: of two tokens with one

@@ -6,6 +6,13 @@
 
 namespace kq8 {
 
+// max that is NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 // roundf(x / d) for the elements of a row whose step is d, |x / d| < 128, with
 // r = RN(1 / d).  r and the product q = RN(x * r) each round once (relative
 // 2^-24), so |q - x / d| <= 128 * 2^-23 and |fl(x / d) - x / d| <= 2^-18:
@@ -24,13 +31,17 @@ namespace kq8 {
 __device__ __forceinline__ uint32_t quantize4(const float4 x, float d, float r, float lo, float hi,
                                               int off) {
     const float magic = 12582912.0f + (float)off;  // 1.5 * 2^23 + off
-    const float q0 = __fmul_rn(x.x, r), q1 = __fmul_rn(x.y, r);
-    const float q2 = __fmul_rn(x.z, r), q3 = __fmul_rn(x.w, r);
-    const float t0 = __fadd_rn(q0, magic), t1 = __fadd_rn(q1, magic);
-    const float t2 = __fadd_rn(q2, magic), t3 = __fadd_rn(q3, magic);
-    const float far = 0.5f - 0x1p-14f;  // NaN / inf compare false
-    const bool ok = fabsf(q0 - (t0 - magic)) < far && fabsf(q1 - (t1 - magic)) < far &&
-                    fabsf(q2 - (t2 - magic)) < far && fabsf(q3 - (t3 - magic)) < far;
+    const float2 r2 = make_float2(r, r), mg = make_float2(magic, magic);
+    const float2 qa = __fmul2_rn(make_float2(x.x, x.y), r2), qb = __fmul2_rn(make_float2(x.z, x.w), r2);
+    const float2 ta = __fadd2_rn(qa, mg), tb = __fadd2_rn(qb, mg);
+    // q - (t - magic), both differences exact where they matter
+    const float2 neg = make_float2(-magic, -magic), minus = make_float2(-1.0f, -1.0f);
+    const float2 da = __ffma2_rn(__fadd2_rn(ta, neg), minus, qa);
+    const float2 db = __ffma2_rn(__fadd2_rn(tb, neg), minus, qb);
+    const float far = 0.5f - 0x1p-14f;
+    const float most = max_nan(max_nan(fabsf(da.x), fabsf(da.y)), max_nan(fabsf(db.x), fabsf(db.y)));
+    const bool ok = most < far;  // NaN / inf compare false
+    const float t0 = ta.x, t1 = ta.y, t2 = tb.x, t3 = tb.y;
     if (ok)
         return __byte_perm(__byte_perm(__float_as_uint(t0), __float_as_uint(t1), 0x0040),
                            __byte_perm(__float_as_uint(t2), __float_as_uint(t3), 0x0040), 0x5410);

@@ -9,10 +9,17 @@
 // that the block touches it touches whole.  Within the block, group i of lanes
 // takes token krow(i): the groups of a warp then hold K rows at adjacent
 // positions of the sub-tile (32 bytes per position and element block).  A lane
-// holds 8 consecutive elements per chunk: one 16-byte access of a 16-bit row
-// (two of an fp32 row) and one 8-byte (q4: 4-byte) access of the pool, so a
-// packed q4 word (elements e .. e + 3 low, e + 4 .. e + 7 high) never crosses
+// holds 8 consecutive elements per chunk: one 16-byte access of a 16-bit row (one
+// of 32 bytes of an fp32 row) and one 8-byte (q4: 4-byte) access of the pool, so
+// a packed q4 word (elements e .. e + 3 low, e + 4 .. e + 7 high) never crosses
 // lanes.  Both are bound by HBM: nothing is read or written twice.
+//
+// Measured, 8 KV heads, against a copy's 6.8 TB/s: fp32, 32768 tokens: write 52 us
+// = 6.4 TB/s, read 55 us = 6.1 (68 with two 16-byte stores a lane, which fill half
+// a sector row each).  bf16, 131072 tokens: read 127 us = 6.4 TB/s, write 166 us =
+// 4.9: the absolute maximum, the division's reciprocal and the rounding of a row
+// cost what an fp32 row's do while the bytes are half.  q4, 131072: read 104 us =
+// 6.5, write 182 us = 3.7.  One token, or 64: 7.5 us, a launch's latency.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -33,56 +40,102 @@ struct Elem8 {
     float4 a, b;
 };
 
-// 8 consecutive elements as fp32 (exact), and back with one rounding each.
-// VEC: 16-byte accesses (p is 16-byte aligned); else element by element.
+// 8 consecutive elements as they lie in memory, one 16-byte word (fp32: two).
+// VEC: p is aligned to their 16 (32) bytes; else element by element.
 template <typename E>
-__device__ __forceinline__ float to_f32(E x);
-template <>
-__device__ __forceinline__ float to_f32(float x) { return x; }
-template <>
-__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
-template <>
-__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
-template <typename E>
-__device__ __forceinline__ E from_f32(float x);
-template <>
-__device__ __forceinline__ float from_f32(float x) { return x; }
-template <>
-__device__ __forceinline__ __half from_f32(float x) { return __float2half_rn(x); }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f32(float x) { return __float2bfloat16_rn(x); }
-
+struct Raw8 {
+    static constexpr int W = (int)sizeof(E) * 8 / 16;
+    uint4 w[W];
+};
 template <typename E, bool VEC>
-__device__ __forceinline__ Elem8 load8(const E* p) {
-    constexpr int W = (int)sizeof(E) * 8 / 16;  // 16-byte words
+__device__ __forceinline__ Raw8<E> load8(const E* p) {
     union {
-        uint4 w[W];
+        Raw8<E> r;
         E e[8];
     } u;
     if constexpr (VEC) {
-#pragma unroll
-        for (int i = 0; i < W; i++) u.w[i] = __ldcs(reinterpret_cast<const uint4*>(p) + i);
+        if constexpr (sizeof(E) == 4)
+            asm volatile("ld.global.cs.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                         : "=r"(u.r.w[0].x), "=r"(u.r.w[0].y), "=r"(u.r.w[0].z), "=r"(u.r.w[0].w),
+                           "=r"(u.r.w[1].x), "=r"(u.r.w[1].y), "=r"(u.r.w[1].z), "=r"(u.r.w[1].w)
+                         : "l"(p));
+        else
+            u.r.w[0] = __ldcs(reinterpret_cast<const uint4*>(p));
     } else {
 #pragma unroll
         for (int i = 0; i < 8; i++) u.e[i] = p[i];
     }
-    Elem8 r;
-    r.a = make_float4(to_f32(u.e[0]), to_f32(u.e[1]), to_f32(u.e[2]), to_f32(u.e[3]));
-    r.b = make_float4(to_f32(u.e[4]), to_f32(u.e[5]), to_f32(u.e[6]), to_f32(u.e[7]));
+    return u.r;
+}
+__device__ __forceinline__ float2 pair_f32(uint32_t w, __half) { return h2_to_f2(w); }
+__device__ __forceinline__ float2 pair_f32(uint32_t w, __nv_bfloat16) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+// As fp32 (exact).
+template <typename E>
+__device__ __forceinline__ Elem8 widen(const Raw8<E>& r) {
+    Elem8 x;
+    if constexpr (sizeof(E) == 4) {
+        x.a = *reinterpret_cast<const float4*>(&r.w[0]);
+        x.b = *reinterpret_cast<const float4*>(&r.w[1]);
+    } else {
+        const float2 p = pair_f32(r.w[0].x, E()), q = pair_f32(r.w[0].y, E());
+        const float2 s = pair_f32(r.w[0].z, E()), t = pair_f32(r.w[0].w, E());
+        x.a = make_float4(p.x, p.y, q.x, q.y);
+        x.b = make_float4(s.x, s.y, t.x, t.y);
+    }
+    return x;
+}
+// max |x| of the 8, NaN ignored as by fmaxf; 16-bit elements in pairs.
+__device__ __forceinline__ uint32_t pair_max(uint32_t a, uint32_t b, __half) {
+    uint32_t r;
+    asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a & 0x7FFF7FFFu), "r"(b & 0x7FFF7FFFu));
     return r;
+}
+__device__ __forceinline__ uint32_t pair_max(uint32_t a, uint32_t b, __nv_bfloat16) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a & 0x7FFF7FFFu), "r"(b & 0x7FFF7FFFu));
+    return r;
+}
+template <typename E>
+__device__ __forceinline__ float max8(const Raw8<E>& r) {
+    if constexpr (sizeof(E) == 4) {
+        const Elem8 x = widen<E>(r);
+        return fmaxf(absmax4(x.a), absmax4(x.b));
+    } else {
+        const uint32_t m = pair_max(pair_max(r.w[0].x, r.w[0].y, E()),
+                                    pair_max(r.w[0].z, r.w[0].w, E()), E());
+        const float2 f = pair_f32(m, E());
+        return fmaxf(fmaxf(f.x, f.y), 0.0f);  // (four NaN pairs)
+    }
+}
+// Stored with one rounding each.
+__device__ __forceinline__ uint32_t pair_of(float x, float y, __half) { return f2_to_h2(x, y); }
+__device__ __forceinline__ uint32_t pair_of(float x, float y, __nv_bfloat16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&v);
 }
 template <typename E, bool VEC>
 __device__ __forceinline__ void store8(E* p, const float (&x)[8]) {
-    constexpr int W = (int)sizeof(E) * 8 / 16;
     union {
-        uint4 w[W];
+        Raw8<E> r;
         E e[8];
     } u;
+    if constexpr (sizeof(E) == 4) {
 #pragma unroll
-    for (int i = 0; i < 8; i++) u.e[i] = from_f32<E>(x[i]);
-    if constexpr (VEC) {
-#pragma unroll
-        for (int i = 0; i < W; i++) __stcs(reinterpret_cast<uint4*>(p) + i, u.w[i]);
+        for (int i = 0; i < 8; i++) u.e[i] = x[i];
+    } else {
+        u.r.w[0] = make_uint4(pair_of(x[0], x[1], E()), pair_of(x[2], x[3], E()),
+                              pair_of(x[4], x[5], E()), pair_of(x[6], x[7], E()));
+    }
+    if constexpr (VEC && sizeof(E) == 4) {
+        // whole 32-byte sectors: two 16-byte stores a lane apart in a row half fill them
+        asm volatile("st.global.cs.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p),
+                     "r"(u.r.w[0].x), "r"(u.r.w[0].y), "r"(u.r.w[0].z), "r"(u.r.w[0].w),
+                     "r"(u.r.w[1].x), "r"(u.r.w[1].y), "r"(u.r.w[1].z), "r"(u.r.w[1].w)
+                     : "memory");
+    } else if constexpr (VEC) {
+        __stcs(reinterpret_cast<uint4*>(p), u.r.w[0]);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; i++) p[i] = u.e[i];
@@ -106,27 +159,16 @@ __device__ __forceinline__ size_t v_off(int32_t page, int h, int nkv, int kv_bs,
     return (page_head(page, h, nkv) * (size_t)kv_bs + (size_t)r) * ROW + (BITS == 8 ? e : e / 2);
 }
 
-// The token, slot and checks shared by write and read: false where the group
-// has nothing to do.  Every lane of a group gets the same answer.
-struct RowAt {
-    int64_t t;
-    int32_t page;
-    int r, h, j;
-};
-__device__ __forceinline__ bool row_at(const RowsParams& P, RowAt& a) {
-    const int grp = threadIdx.x / RW_LPR;
-    a.j = threadIdx.x % RW_LPR;
-    a.h = blockIdx.y;
-    a.t = (int64_t)blockIdx.x * TILE + krow(grp);
-    if (a.t >= P.T) return false;
-    const int32_t sl = __ldg(P.slot + a.t);
+// Where a slot is: page and row; false (and a status bit for a slot past the pool)
+// where there is nothing to do.  Every lane of a group gets the same answer.
+__device__ __forceinline__ bool slot_at(const RowsParams& P, int32_t sl, int32_t& page, int& r) {
     if (sl < 0) return false;
     if ((int64_t)sl >= (int64_t)P.cache.num_pages * P.cache.kv_bs) {
-        if (a.j == 0 && P.status) atomicOr(P.status, KQ8_STATUS_BAD_SLOT);
+        if (threadIdx.x % RW_LPR == 0 && P.status) atomicOr(P.status, KQ8_STATUS_BAD_SLOT);
         return false;
     }
-    a.page = sl / P.cache.kv_bs;
-    a.r = sl - a.page * P.cache.kv_bs;
+    page = sl / P.cache.kv_bs;
+    r = sl - page * P.cache.kv_bs;
     return true;
 }
 
@@ -146,100 +188,153 @@ __device__ __forceinline__ void put_codes(int8_t* dst, const Elem8& x, float d, 
 }
 
 // The write rule on the row widened to fp32, so the codes and maxima equal
-// kq8_append_kv's for the same values bit for bit.
-template <typename E, int BITS, bool VEC>
+// kq8_append_kv's for the same values bit for bit.  The rows are fetched beside
+// their slots; a block takes NT sub-tiles of 32 tokens, all fetched before the first
+// is quantised.
+template <typename E, int BITS, bool VEC, int NT>
 __global__ void __launch_bounds__(RW_THREADS) kq8_write_kernel(const RowsParams P) {
     griddep_wait();
     griddep_launch_dependents();
-    RowAt at;
-    const bool on = row_at(P, at);
-    Elem8 x[2][RW_NC];
-    float m[2] = {0.0f, 0.0f};
-    if (on) {
-        const E* src[2] = {
-            static_cast<const E*>(P.k) + at.t * P.k_st + at.h * P.k_sh,
-            static_cast<const E*>(P.v) + at.t * P.v_st + at.h * P.v_sh};
-#pragma unroll
-        for (int s = 0; s < 2; s++)
-#pragma unroll
-            for (int i = 0; i < RW_NC; i++)
-                x[s][i] = load8<E, VEC>(src[s] + 8 * (RW_LPR * i + at.j));
-#pragma unroll
-        for (int s = 0; s < 2; s++)
-#pragma unroll
-            for (int i = 0; i < RW_NC; i++)
-                m[s] = fmaxf(m[s], fmaxf(absmax4(x[s][i].a), absmax4(x[s][i].b)));
-    }
-#pragma unroll
-    for (int o = 1; o < RW_LPR; o <<= 1)
-#pragma unroll
-        for (int s = 0; s < 2; s++) m[s] = fmaxf(m[s], __shfl_xor_sync(0xffffffffu, m[s], o));
-    if (!on) return;
+    const int j = threadIdx.x % RW_LPR, h = blockIdx.y;
+    const int64_t t0 = (int64_t)blockIdx.x * (NT * TILE) + krow(threadIdx.x / RW_LPR);
     const int nkv = P.cache.num_kv_heads, kv_bs = P.cache.kv_bs;
+    int32_t slot[NT];
+    Raw8<E> x[NT][2][RW_NC];
 #pragma unroll
-    for (int s = 0; s < 2; s++) {
-        const float d = __fmul_rn(m[s], BITS == 8 ? inv127() : inv7()), r = __frcp_rn(d);
+    for (int n = 0; n < NT; n++) {
+        const int64_t t = t0 + n * TILE;
+        slot[n] = t < P.T ? __ldg(P.slot + t) : -1;
+        if (t < P.T) {
+            const E* k = static_cast<const E*>(P.k) + t * P.k_st + h * P.k_sh;
+            const E* v = static_cast<const E*>(P.v) + t * P.v_st + h * P.v_sh;
 #pragma unroll
-        for (int i = 0; i < RW_NC; i++) {
-            const int e = 8 * (RW_LPR * i + at.j);
-            int8_t* dst = s == 0 ? P.cache.k + k_off<BITS>(at.page, at.h, nkv, kv_bs, at.r, e)
-                                 : P.cache.v + v_off<BITS>(at.page, at.h, nkv, kv_bs, at.r, e);
-            put_codes<BITS>(dst, x[s][i], d, r, m[s] == 0.0f);
+            for (int i = 0; i < RW_NC; i++) {
+                x[n][0][i] = load8<E, VEC>(k + 8 * (RW_LPR * i + j));
+                x[n][1][i] = load8<E, VEC>(v + 8 * (RW_LPR * i + j));
+            }
+        } else {
+#pragma unroll
+            for (int s = 0; s < 2; s++)
+#pragma unroll
+                for (int i = 0; i < RW_NC; i++)
+#pragma unroll
+                    for (int w = 0; w < Raw8<E>::W; w++) x[n][s][i].w[w] = make_uint4(0u, 0u, 0u, 0u);
         }
     }
-    if (at.j == 0) {
-        const size_t so = page_head(at.page, at.h, nkv) * (size_t)kv_bs + at.r;
-        P.cache.kscale[so] = m[0];
-        P.cache.vscale[so] = m[1];
+#pragma unroll
+    for (int n = 0; n < NT; n++) {
+        float m[2];
+#pragma unroll
+        for (int s = 0; s < 2; s++) {
+            m[s] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < RW_NC; i++) m[s] = fmaxf(m[s], max8<E>(x[n][s][i]));
+#pragma unroll
+            for (int o = 1; o < RW_LPR; o <<= 1)
+                m[s] = fmaxf(m[s], __shfl_xor_sync(0xffffffffu, m[s], o));
+        }
+        int32_t page;
+        int r;
+        if (!slot_at(P, slot[n], page, r)) continue;
+#pragma unroll
+        for (int s = 0; s < 2; s++) {
+            const float d = __fmul_rn(m[s], BITS == 8 ? inv127() : inv7()), rcp = __frcp_rn(d);
+#pragma unroll
+            for (int i = 0; i < RW_NC; i++) {
+                const int e = 8 * (RW_LPR * i + j);
+                int8_t* dst = s == 0 ? P.cache.k + k_off<BITS>(page, h, nkv, kv_bs, r, e)
+                                     : P.cache.v + v_off<BITS>(page, h, nkv, kv_bs, r, e);
+                put_codes<BITS>(dst, widen<E>(x[n][s][i]), d, rcp, m[s] == 0.0f);
+            }
+        }
+        if (j == 0) {
+            const size_t so = page_head(page, h, nkv) * (size_t)kv_bs + r;
+            P.cache.kscale[so] = m[0];
+            P.cache.vscale[so] = m[1];
+        }
     }
 }
 
-// 8 codes -> 8 fp32 values (exact).
+// 8 codes as stored, and as fp32 (exact).
 template <int BITS>
-__device__ __forceinline__ void get_codes(const int8_t* src, float (&c)[8]) {
+struct Codes8 {
+    uint32_t w[BITS == 8 ? 2 : 1];
+};
+template <int BITS>
+__device__ __forceinline__ Codes8<BITS> get_codes(const int8_t* src) {
+    Codes8<BITS> c;
     if constexpr (BITS == 8) {
         const uint2 w = __ldcs(reinterpret_cast<const uint2*>(src));
-        i8x4_to_f32(w.x, c[0], c[1], c[2], c[3]);
-        i8x4_to_f32(w.y, c[4], c[5], c[6], c[7]);
+        c.w[0] = w.x;
+        c.w[1] = w.y;
     } else {
-        const uint32_t w = __ldcs(reinterpret_cast<const uint32_t*>(src));
+        c.w[0] = __ldcs(reinterpret_cast<const uint32_t*>(src));
+    }
+    return c;
+}
+template <int BITS>
+__device__ __forceinline__ void code_values(const Codes8<BITS>& c, float (&y)[8]) {
+    if constexpr (BITS == 8) {
+        i8x4_to_f32(c.w[0], y[0], y[1], y[2], y[3]);
+        i8x4_to_f32(c.w[1], y[4], y[5], y[6], y[7]);
+    } else {
 #pragma unroll
         for (int i = 0; i < 8; i++)
-            c[i] = (float)((int)((w >> (8 * (i & 3) + 4 * (i >> 2))) & 15u) - 8);
+            y[i] = (float)((int)((c.w[0] >> (8 * (i & 3) + 4 * (i >> 2))) & 15u) - 8);
     }
 }
 
 // The values the rows stand for: code * (stored max * (1/127)) (q4: 1/7), one
 // fp32 product as the attention kernels' readers form it, then one rounding to
-// the output type.
-template <typename E, int BITS, bool VEC>
+// the output type.  NT as for the write.
+template <typename E, int BITS, bool VEC, int NT>
 __global__ void __launch_bounds__(RW_THREADS) kq8_read_kernel(const RowsParams P) {
     griddep_wait();
     griddep_launch_dependents();
-    RowAt at;
-    if (!row_at(P, at)) return;
+    const int j = threadIdx.x % RW_LPR, h = blockIdx.y;
+    const int64_t t0 = (int64_t)blockIdx.x * (NT * TILE) + krow(threadIdx.x / RW_LPR);
     const int nkv = P.cache.num_kv_heads, kv_bs = P.cache.kv_bs;
-    const size_t so = page_head(at.page, at.h, nkv) * (size_t)kv_bs + at.r;
-    float c[2][RW_NC][8];
+    int32_t slot[NT];
 #pragma unroll
-    for (int i = 0; i < RW_NC; i++) {
-        const int e = 8 * (RW_LPR * i + at.j);
-        get_codes<BITS>(P.cache.k + k_off<BITS>(at.page, at.h, nkv, kv_bs, at.r, e), c[0][i]);
-        get_codes<BITS>(P.cache.v + v_off<BITS>(at.page, at.h, nkv, kv_bs, at.r, e), c[1][i]);
-    }
-    const float inv = BITS == 8 ? inv127() : inv7();
-    const float d[2] = {__fmul_rn(P.cache.kscale[so], inv), __fmul_rn(P.cache.vscale[so], inv)};
-    E* dst[2] = {static_cast<E*>(P.k) + at.t * P.k_st + at.h * P.k_sh,
-                 static_cast<E*>(P.v) + at.t * P.v_st + at.h * P.v_sh};
+    for (int n = 0; n < NT; n++) slot[n] = t0 + n * TILE < P.T ? __ldg(P.slot + t0 + n * TILE) : -1;
+    bool on[NT];
+    Codes8<BITS> c[NT][2][RW_NC];
+    float m[NT][2];
 #pragma unroll
-    for (int s = 0; s < 2; s++)
+    for (int n = 0; n < NT; n++) {
+        int32_t page;
+        int r;
+        on[n] = slot_at(P, slot[n], page, r);
+        if (!on[n]) continue;
 #pragma unroll
         for (int i = 0; i < RW_NC; i++) {
-            float y[8];
-#pragma unroll
-            for (int k = 0; k < 8; k++) y[k] = __fmul_rn(c[s][i][k], d[s]);
-            store8<E, VEC>(dst[s] + 8 * (RW_LPR * i + at.j), y);
+            const int e = 8 * (RW_LPR * i + j);
+            c[n][0][i] = get_codes<BITS>(P.cache.k + k_off<BITS>(page, h, nkv, kv_bs, r, e));
+            c[n][1][i] = get_codes<BITS>(P.cache.v + v_off<BITS>(page, h, nkv, kv_bs, r, e));
         }
+        const size_t so = page_head(page, h, nkv) * (size_t)kv_bs + r;
+        m[n][0] = P.cache.kscale[so];
+        m[n][1] = P.cache.vscale[so];
+    }
+#pragma unroll
+    for (int n = 0; n < NT; n++) {
+        if (!on[n]) continue;
+        const int64_t t = t0 + n * TILE;
+        E* dst[2] = {static_cast<E*>(P.k) + t * P.k_st + h * P.k_sh,
+                     static_cast<E*>(P.v) + t * P.v_st + h * P.v_sh};
+#pragma unroll
+        for (int s = 0; s < 2; s++) {
+            const float d = __fmul_rn(m[n][s], BITS == 8 ? inv127() : inv7());
+#pragma unroll
+            for (int i = 0; i < RW_NC; i++) {
+                float y[8];
+                code_values<BITS>(c[n][s][i], y);
+#pragma unroll
+                for (int k = 0; k < 8; k++) y[k] = __fmul_rn(y[k], d);
+                store8<E, VEC>(dst[s] + 8 * (RW_LPR * i + j), y);
+            }
+        }
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -321,15 +416,27 @@ __global__ void __launch_bounds__(CM_THREADS) kq8_commit_kernel(const CommitPara
     }
 }
 
+template <bool WRITE, typename E, int BITS, bool VEC, int NT>
+int launch_rows_n(const RowsParams& p, cudaStream_t s) {
+    const dim3 grid((unsigned)(((int64_t)p.T + NT * TILE - 1) / (NT * TILE)),
+                    (unsigned)p.cache.num_kv_heads);
+    if constexpr (WRITE)
+        return launch_pdl(kq8_write_kernel<E, BITS, VEC, NT>, grid, RW_THREADS, s, p);
+    else
+        return launch_pdl(kq8_read_kernel<E, BITS, VEC, NT>, grid, RW_THREADS, s, p);
+}
 template <bool WRITE, typename E, int BITS>
 int launch_rows_t(const RowsParams& p, bool vec, cudaStream_t s) {
-    const dim3 grid((unsigned)(((int64_t)p.T + TILE - 1) / TILE), (unsigned)p.cache.num_kv_heads);
-    if constexpr (WRITE)
-        return vec ? launch_pdl(kq8_write_kernel<E, BITS, true>, grid, RW_THREADS, s, p)
-                   : launch_pdl(kq8_write_kernel<E, BITS, false>, grid, RW_THREADS, s, p);
-    else
-        return vec ? launch_pdl(kq8_read_kernel<E, BITS, true>, grid, RW_THREADS, s, p)
-                   : launch_pdl(kq8_read_kernel<E, BITS, false>, grid, RW_THREADS, s, p);
+    if (!vec) return launch_rows_n<WRITE, E, BITS, false, 1>(p, s);
+    // A bulk read of 16-bit rows takes two sub-tiles a block, their loads in flight
+    // together (131072 tokens, 8 KV heads, bf16: 141 us with one, 127 with two, 149 with
+    // four).  A small one has too few blocks for that; a write holds more registers per
+    // sub-tile (183, 212, 303 us), fp32 rows and q4 codes gain nothing.
+    if constexpr (!WRITE && BITS == 8 && sizeof(E) == 2) {
+        const int64_t blocks = ((int64_t)p.T + TILE - 1) / TILE * p.cache.num_kv_heads;
+        if (blocks >= (int64_t)device_sms() * 16) return launch_rows_n<WRITE, E, BITS, true, 2>(p, s);
+    }
+    return launch_rows_n<WRITE, E, BITS, true, 1>(p, s);
 }
 
 template <bool WRITE, int BITS>
@@ -350,8 +457,8 @@ bool rows_apart(int64_t s1, int64_t n1, int64_t s2, int64_t n2) {
     return s1 >= HD && s2 >= (n1 - 1) * s1 + HD;
 }
 
-// Checks, the choice of 16-byte accesses (bases and strides multiples of 16
-// bytes), launch.
+// Checks, the choice of vector accesses (bases and strides multiples of 8
+// elements), launch.
 template <bool WRITE>
 int rows_impl(const kq8_cache_t* cache, int32_t bits, void* k, void* v, int32_t dtype,
               size_t k_st, size_t k_sh, size_t v_st, size_t v_sh, const int32_t* slot, int32_t T, uint32_t* status, kq8_stream_t stream) {
@@ -367,10 +474,11 @@ int rows_impl(const kq8_cache_t* cache, int32_t bits, void* k, void* v, int32_t 
         return KQ8_ERR_INVALID_ARG;
     if (status && (uintptr_t)status % 4) return KQ8_ERR_INVALID_ARG;
     const size_t st[4] = {k_st, k_sh, v_st, v_sh};
-    bool vec = (uintptr_t)k % 16 == 0 && (uintptr_t)v % 16 == 0;
+    const size_t chunk = 8 * es;  // what a lane moves at a time
+    bool vec = (uintptr_t)k % chunk == 0 && (uintptr_t)v % chunk == 0;
     for (size_t x : st) {
         if (x > MAX_STRIDE) return KQ8_ERR_INVALID_ARG;
-        vec = vec && (x * es) % 16 == 0;
+        vec = vec && (x * es) % chunk == 0;
     }
     // the rows a read stores must not overlap
     const int64_t heads = cache->num_kv_heads;
