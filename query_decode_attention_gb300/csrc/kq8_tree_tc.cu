@@ -11,13 +11,19 @@
 // own.  bf16 outputs, whose own rounding is 2^-9, take Q and P at 11 bits, and K and V
 // already multiplied by their token's scale (relative to a power of two per 32 tokens),
 // 11 bits too: that leaves the softmax one multiply-add and one exponential per score
-// instead of two loads and three operations (a step of one tile 5500 -> @@ cycles).
+// instead of two loads and three operations (128 rows of 16 x 16384 tokens: 350 us with
+// the scales beside the softmax, 296 with them in the operands).
 //
 // What bounds it.  Per 128-token step shared memory carries the raw bytes in and out of
 // the ring (66 KB), the widened operands in (64 KB) and, per tile, Q and K (64 KB) and V
 // (32 KB) to the MMAs: 226 KB for one tile, 322 KB for two or for hi and lo, 1770 and
 // 2520 cycles at 128 bytes; the MMAs themselves take 1024 and 2048 (64 each), HBM 1440
-// for the step's 33 KB.  With few rows the mma.sync kernel moves less: see tree_plan.
+// for the step's 33 KB.  Measured, 16 x 16384 tokens, 8 KV heads (83 us of HBM): 128
+// rows bf16 221 us, 256 rows 342, 128 rows fp32 326: 3900, 6000 and 5700 cycles a step.
+// The schedulers issue in half of the cycles; what is left is the latency of the chain
+// widen K -> S -> widen K and of the roles' own code (steps of 64 tokens and K's and V's
+// raw bytes in rings of their own, which loosen the chain, gained nothing: 390 and 226
+// us at 128 rows).  With few rows the mma.sync kernel moves less: see tree_plan.
 //
 // One persistent CTA per SM takes an equal share of all steps: the lists (row tile, KV
 // head, sequence) lie one behind the other and are cut where a share ends, so ragged
@@ -25,16 +31,21 @@
 // output, the pieces of a cut one to a merge kernel.  Two streams of steps keep the
 // tensor core and the softmax busy at once: with two tiles (T = 2) each tile is a
 // stream; with one, the even steps are one stream and the odd steps the other, each
-// with its own O, reference and sum, joined at a list's end.  With hi and lo parts there
-// is one stream (TMEM: O 128 columns, S 2 x 128, P 128), else TMEM holds O 2 x 128, S 128
-// for both in turn, P 2 x 64.  Roles, which meet on mbarriers:
+// with its own O, reference and sum, joined at a list's end (fp32, 128 rows: 359 us with
+// one stream, 334 with two).  TMEM holds O 2 x 128 columns and S 2 x 128, the weights
+// over the scores.  Roles, which meet on mbarriers:
 //   warps 0-3, 4-7  softmax of stream 0, 1, one thread per row (TMEM lane), as in
 //                   kq8_prompt.cu; the reference m refers to weights (score + log2 of
 //                   the V step), so that they fit fp16 whatever the V steps are;
-//   warps 8-11      widen one 32-token sub-tile each of a step to fp16, K then V;
-//   warp 12         one lane issues S, the streams in turn;
-//   warps 13, 14    one lane each issues PV of stream 0, 1;
-//   warp 15         copies raw sub-tiles (codes and scales) into a ring.
+//   warps 8-11      widen one 32-token sub-tile of K each of a step to fp16;
+//   warps 12-15     the same of V;
+//   warp 16         one lane issues S, the streams in turn;
+//   warps 17, 18    one lane each issues PV of a tile (of one tile: 17, the streams in
+//                   turn);
+//   warp 19         copies raw sub-tiles (codes and scales) into a ring.
+// A list's start is on every share's path: its Q is quantised 8 lanes to a row with the
+// loads of 8 rows in flight (a row at a time by a whole warp: 268 us at 128 rows and 402
+// at 256 instead of 221 and 342).
 // Order of tokens.  Row r of a 32-token sub-tile's operands holds K position rho(r)
 // (bits 1 and 2 swapped), token krow(rho(r)): with it the copies from the raw tile
 // (contiguous 512 bytes an instruction) to the swizzled operand rows are free of bank
@@ -61,13 +72,14 @@ template <int T, bool HILO>
 struct TcShape {
     static_assert(T == 1 || !HILO, "hi and lo parts of one tile");
     static constexpr int NR = 128 * T;                 // rows of a list
-    static constexpr int NS = HILO ? 1 : 2;            // streams
     // Rings, as far as shared memory goes.  A parity wait is only sound for a waiter
     // that waits for every phase of a barrier, in order: so the raw ring is a multiple
-    // of four long (a place has the same two consumers, sub-tile w's K and V warp), and
-    // with one tile and two streams V has two places, one per stream (stream = step % 2).
-    static constexpr int RAWN = 8, VB = T == 1 && !HILO ? 2 : 1;
-    static constexpr uint32_t Q = 0, K = (T + (HILO ? 1 : 0)) * TC_OP, V = K + TC_OP,
+    // of four long (a place has the same two consumers, sub-tile w's K and V warp).
+    // One tile and one part leave room for a second place of K or of V; V's it is:
+    // 128 rows of 16 x 16384 tokens take 268 us so, 292 with K's.  Raw places given up
+    // for either cost more than it gains.
+    static constexpr int RAWN = 8, KB = 1, VB = T == 1 && !HILO ? 2 : 1;
+    static constexpr uint32_t Q = 0, K = (T + (HILO ? 1 : 0)) * TC_OP, V = K + KB * TC_OP,
                               RAW = V + VB * TC_OP,
                               SC = RAW + RAWN * STAGE_BYTES,  // [4][3][128] floats
                               // [4][4]: something is missing or not finite, a bound of log2
@@ -78,11 +90,10 @@ struct TcShape {
                               MISC = EX + 2048,               // TMEM, abort, flags, share
                               BAR = MISC + 128, SMEM = BAR + 512 + 1024;
     // barriers
-    static constexpr int B_RAWF = 0, B_RAWE = B_RAWF + RAWN, B_KF = B_RAWE + RAWN, B_KE = B_KF + 1,
-                         B_VF = B_KE + 1, B_VE = B_VF + VB, B_SCF = B_VE + VB,
-                         B_SF = B_SCF + 4,   // [stream], hi and lo: [S buffer]
-                         B_SR = B_SF + 2,    // hi and lo: S has been read, [S buffer]
-                         B_P = B_SR + 2,     // [stream][half]
+    static constexpr int B_RAWF = 0, B_RAWE = B_RAWF + RAWN, B_KF = B_RAWE + RAWN,
+                         B_KE = B_KF + KB, B_VF = B_KE + KB, B_VE = B_VF + VB, B_SCF = B_VE + VB,
+                         B_SF = B_SCF + 4,   // [stream]
+                         B_P = B_SF + 2,     // [stream][half]
                          B_PV = B_P + 4,     // [stream]
                          B_QF = B_PV + 2, B_XF = B_QF + 1, B_XE = B_XF + 1,
                          B_FINAL = B_XE + 1, B_COUNT = B_FINAL + 3;
@@ -213,8 +224,8 @@ template <int T, bool HILO>
 __global__ void __launch_bounds__(TC_THREADS, 1)
     kq8_tree_tc_kernel(const __grid_constant__ TreeParams P) {
     using Sh = TcShape<T, HILO>;
-    constexpr int NR = Sh::NR, NS = Sh::NS, RAWN = Sh::RAWN, VB = Sh::VB;
-    constexpr bool SPLIT = T == 1 && !HILO;  // the streams are the even and the odd steps
+    constexpr int NR = Sh::NR, RAWN = Sh::RAWN, KB = Sh::KB, VB = Sh::VB;
+    constexpr bool SPLIT = T == 1;  // the streams are the even and the odd steps
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -231,11 +242,12 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         for (int i = 0; i < Sh::B_COUNT; i++) {
             uint32_t cnt = 1;
             if (i >= Sh::B_RAWE && i < Sh::B_KF) cnt = 2;
-            if (i == Sh::B_KF || (i >= Sh::B_VF && i < Sh::B_VE)) cnt = 4;
+            if (i >= Sh::B_KF && i < Sh::B_KE) cnt = 4;
+            if (i >= Sh::B_VF && i < Sh::B_VE) cnt = 4;
             if (i >= Sh::B_VE && i < Sh::B_SCF) cnt = T;  // a PV thread per tile
             if (i >= Sh::B_SCF && i < Sh::B_SF) cnt = 4;
-            if (i >= Sh::B_SR && i < Sh::B_PV) cnt = 4;   // SR and P
-            if (i >= Sh::B_QF && i < Sh::B_FINAL) cnt = 4 * NS;
+            if (i >= Sh::B_P && i < Sh::B_PV) cnt = 4;
+            if (i >= Sh::B_QF && i < Sh::B_FINAL) cnt = 8;
             mbar_init(bars + i, cnt);
         }
         *abort_flag = 0;
@@ -278,10 +290,11 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     float* sc = reinterpret_cast<float*>(sm + Sh::SC);
     float4* meta = reinterpret_cast<float4*>(sm + Sh::META);
     float* rf_sm = reinterpret_cast<float*>(sm + Sh::RF);
-    // TMEM columns
+    // TMEM columns: O, the scores and, over them, the weights (of 16 tokens; lo 16 columns
+    // on, so that a chunk of 32 tokens stays within its scores)
     auto col_o = [&](int t) { return tbase + 128 * t; };
-    auto col_s = [&](int t, uint32_t n) { return tbase + (HILO ? 128 + 128 * (n & 1) : 256 + 128 * t); };
-    auto col_p = [&](int t) { return tbase + (HILO ? 384 : 256 + 128 * t); };  // lo: 64 on
+    auto col_s = [&](int t) { return tbase + 256 + 128 * t; };
+    auto off_p = [](int kk) { return HILO ? 32 * (kk >> 1) + 8 * (kk & 1) : 8 * kk; };
 
     if (warp >= TC_W_S) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(TC_REGS_REST));
@@ -356,17 +369,13 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             while (ok && walk.next(P, NR, it)) {
                 ok = wait(Sh::B_QF, qn++ & 1);
                 for (int j = 0; ok && j < it.steps; j++, g++) {
-                    if (!(ok = wait(Sh::B_KF, g & 1))) break;
+                    const int place = g % KB;
+                    if (!(ok = wait(Sh::B_KF + place, (g / KB) & 1))) break;
+                    const uint64_t k = dk + (uint64_t)(place * (TC_OP >> 4));
                     for (int i = 0; ok && i < T; i++) {
                         const int t = SPLIT ? (int)(g & 1) : i;
-                        // the place is free: hi and lo, when the scores have been read, else
-                        // when PV has read the weights over them
-                        if (HILO) {
-                            if (n[0] >= 2 && !(ok = wait(Sh::B_SR + (n[0] & 1), ((n[0] - 2) >> 1) & 1)))
-                                break;
-                        } else if (n[t] >= 1 && !(ok = wait(Sh::B_PV + t, (n[t] - 1) & 1))) {
-                            break;
-                        }
+                        // the place is free when PV has read the weights over the scores
+                        if (n[t] >= 1 && !(ok = wait(Sh::B_PV + t, (n[t] - 1) & 1))) break;
                         tc::fence_after_sync();
 #pragma unroll
                         for (int part = 0; part < (HILO ? 2 : 1); part++) {
@@ -374,54 +383,56 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
 #pragma unroll
                             for (int kk = 0; kk < HD / 16; kk++) {
                                 const uint64_t o = (kk >> 2) * (TC_PANEL >> 4) + (kk & 3) * 2;
-                                tc::mma_f16(col_s(t, n[0]), a + o, dk + o, IDS, kk > 0 || part > 0);
+                                tc::mma_f16(col_s(t), a + o, k + o, IDS, kk > 0 || part > 0);
                             }
                         }
-                        tc::mma_commit(bars + Sh::B_SF + (HILO ? n[0] & 1 : t));
+                        tc::mma_commit(bars + Sh::B_SF + t);
                         n[t]++;
                     }
-                    if (ok) tc::mma_commit(bars + Sh::B_KE);
+                    if (ok) tc::mma_commit(bars + Sh::B_KE + place);
                 }
             }
             // every commit has arrived before the CTA may end (bounded)
             tc::mma_commit(bars + Sh::B_FINAL);
             mbar_wait_bounded(bars + Sh::B_FINAL, 0);
-            if (ok && g > 0) mbar_wait_bounded(bars + Sh::B_KE, (g - 1) & 1);
-        } else if (warp >= TC_W_PV && warp < TC_W_PV + NS && lane == 0) {
-            // ---- PV of stream t.  V's step of 16 tokens is two groups of eight rows.
-            const int t = warp - TC_W_PV;
+            for (uint32_t k = g > (uint32_t)KB ? g - KB : 0; ok && k < g; k++)
+                mbar_wait_bounded(bars + Sh::B_KE + k % KB, (k / KB) & 1);
+        } else if (warp >= TC_W_PV && warp < TC_W_PV + T && lane == 0) {
+            // ---- PV, of a tile or of both streams in turn.  V's step of 16 tokens is two
+            // groups of eight rows.
+            const int tile = warp - TC_W_PV;
             const uint64_t dv = tc::sdesc_sw128(smem_u32(sm + Sh::V), TC_PANEL, 1024);
             constexpr uint32_t IDO = tc::IDesc<128, HD, false>::value | tc::IDESC_B_MN;
-            uint32_t g = 0, n = 0;  // steps, this stream's steps so far
+            uint32_t g = 0;            // steps so far
             bool ok = true;
             while (ok && walk.next(P, NR, it)) {
-                bool first = true;
                 for (int j = 0; ok && j < it.steps; j++, g++) {
-                    if (SPLIT && (int)(g & 1) != t) continue;
-                    const int place = SPLIT ? t : 0;
+                    const int place = g % VB, t = SPLIT ? (int)(g & 1) : tile;
+                    const uint32_t m = SPLIT ? g >> 1 : g;  // of the stream
+                    const bool first = j < (SPLIT ? 2 : 1);
                     const uint64_t v = dv + (uint64_t)(place * (TC_OP >> 4));
-                    ok = wait(Sh::B_VF + place, (SPLIT ? g >> 1 : g) & 1);
+                    ok = wait(Sh::B_VF + place, (g / VB) & 1);
 #pragma unroll
                     for (int half = 0; half < 2; half++) {
-                        if (!(ok = ok && wait(Sh::B_P + 2 * t + half, n & 1))) break;
+                        if (!(ok = ok && wait(Sh::B_P + 2 * t + half, m & 1))) break;
                         tc::fence_after_sync();
 #pragma unroll
                         for (int kk = 4 * half; kk < 4 * half + 4; kk++) {
                             const uint64_t b = v + (uint64_t)(kk * (2048 >> 4));
-                            tc::mma_f16_ta(col_o(t), col_p(t) + 8 * kk, b, IDO, !first || kk > 0);
-                            if (HILO) tc::mma_f16_ta(col_o(t), col_p(t) + 64 + 8 * kk, b, IDO, true);
+                            const uint32_t p = col_s(t) + off_p(kk);
+                            tc::mma_f16_ta(col_o(t), p, b, IDO, !first || kk > 0);
+                            if (HILO) tc::mma_f16_ta(col_o(t), p + 16, b, IDO, true);
                         }
                     }
                     if (!ok) break;
-                    first = false;
-                    n++;
                     tc::mma_commit(bars + Sh::B_PV + t);
                     tc::mma_commit(bars + Sh::B_VE + place);
                 }
             }
-            tc::mma_commit(bars + Sh::B_FINAL + 1 + t);
-            mbar_wait_bounded(bars + Sh::B_FINAL + 1 + t, 0);
-            if (ok && n > 0) mbar_wait_bounded(bars + Sh::B_VE + (SPLIT ? t : 0), (n - 1) & 1);
+            tc::mma_commit(bars + Sh::B_FINAL + 1 + tile);
+            mbar_wait_bounded(bars + Sh::B_FINAL + 1 + tile, 0);
+            for (uint32_t k = g > (uint32_t)VB ? g - VB : 0; ok && k < g; k++)
+                mbar_wait_bounded(bars + Sh::B_VE + k % VB, (k / VB) & 1);
         }
     } else if (warp >= TC_W_WIDEN) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(TC_REGS_WIDEN));
@@ -435,7 +446,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         while (ok && walk.next(P, NR, it)) {
             for (int j = 0; j < it.steps; j++, g++) {
                 const uint32_t ri = 4 * g + w;
-                const int s = ri % RAWN, place = VB == 2 ? g & 1 : 0;
+                const int s = ri % RAWN, place = g % (is_v ? VB : KB);
                 if (!(ok = all(wait(Sh::B_RAWF + s, (ri / RAWN) & 1)))) break;
                 const uint8_t* st = sm + Sh::RAW + s * STAGE_BYTES;
                 // lane = operand row: its token's K multiplier or V step
@@ -454,10 +465,10 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                                             ? __float_as_uint(fabsf(km)) : 0u;
                     const int ke = above(__uint_as_float(__reduce_max_sync(0xffffffffu, kb)));
                     const bool odd = !have || __any_sync(0xffffffffu, !(fabsf(vstep) < INFINITY));
-                    if (g > 0 && !(ok = all(wait(Sh::B_KE, (g - 1) & 1)))) break;
-                    // (The place of the step's scales was last read for step g - 4.  S(g - 1),
-                    // which freed K's place, went over scores whose weights PV had read: of
-                    // step g - 3 or g - 2, one stream's, and the other's step came before.)
+                    if (g >= (uint32_t)KB && !(ok = all(wait(Sh::B_KE + place, (g / KB - 1) & 1)))) break;
+                    // (The place of the step's scales was last read for step g - 4.  Before
+                    // S(g - KB) PV had read the weights of step g - KB - 2 and all before it.)
+                    static_assert(KB <= 2, "scales");
                     float* d = sc + (g & 3) * 384 + 32 * w + lane;
                     d[0] = km;
                     d[128] = vstep;
@@ -484,7 +495,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                             xb = *reinterpret_cast<const uint4*>(st + 1024 * (blk + 1) + 512 + 16 * lane);
                         }
                         const int c = (blk & 1) * 4 + (lane & 1) * 2;
-                        uint8_t* o = sm + Sh::K + (blk >> 1) * TC_PANEL + rowa * 128;
+                        uint8_t* o = sm + Sh::K + place * TC_OP + (blk >> 1) * TC_PANEL + rowa * 128;
                         const int c0 = (c ^ x7) << 4, c1 = ((c + 1) ^ x7) << 4;
                         *reinterpret_cast<uint4*>(o + c0) = widen8<HILO>(ya.x, ya.y, fa);
                         *reinterpret_cast<uint4*>(o + c1) = widen8<HILO>(ya.z, ya.w, fa);
@@ -529,7 +540,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                 if (lane == 0) {
                     tc_arrive(bars + Sh::B_RAWE + s);
                     if (!is_v) tc_arrive(bars + Sh::B_SCF + (g & 3));
-                    tc_arrive(bars + (is_v ? Sh::B_VF + place : Sh::B_KF));
+                    tc_arrive(bars + (is_v ? Sh::B_VF : Sh::B_KF) + place);
                 }
             }
         }
@@ -538,10 +549,10 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         const int t = warp >> 2, w4 = warp & 3;  // stream
         const int row = w4 * 32 + lane;          // of its tile
         const uint32_t lanes = (uint32_t)(w4 * 32) << 16;
-        const uint32_t tO = col_o(t) + lanes, tP = col_p(t) + lanes;
+        const uint32_t tO = col_o(t) + lanes, tS = col_s(t) + lanes;
         float2* ex = reinterpret_cast<float2*>(sm + Sh::EX);
         uint32_t g = 0, n = 0, xn = 0;  // steps, this stream's steps, lists so far
-        bool ok = t < NS;
+        bool ok = true;
         for (int piece = 0; ok && walk.next(P, NR, it); piece++) {
             const int tile = T == 2 ? t : 0;
             const int r0 = it.rt * NR + 128 * tile;        // first row of the tile
@@ -549,34 +560,71 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             // ---- Q (article 9-2 §2 seg. 1): codes times block scales, scaled per row.
             // Stream t of a split tile prepares half of it.  (With one tile the streams
             // have met since their last scores, below.)
+            // 8 lanes a row, 16 elements a lane, the loads of 8 rows in flight together.
             constexpr int QR = SPLIT ? 16 : 32;            // rows per warp
-#pragma unroll 4
-            for (int i = 0; i < QR; i++) {
-                const int r = (SPLIT ? 64 * t : 0) + w4 * QR + i;
-                float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                if (r < rows)
-                    x = load_q4(P.q, P.dtype, (int64_t)(it.s.q0 + (r0 + r) / P.G) * P.q_st +
-                                                  (it.h * P.G + (r0 + r) % P.G) * P.q_sh + 4 * lane);
-                float qs;
-                const uint32_t code = quantize_q_lane(x, qs);
-                float top = qs;
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                // 127 * top in [2^13, 2^14) after the scale
-                const int e = min(max((int)(__float_as_uint(top) >> 23) - 127 + 7 - 13, -100), 100);
-                if (lane == 0) rf_sm[128 * tile + r] = pow2i(e);
-                qs *= pow2i(-e);
-                float v[4];
+#pragma unroll 1
+            for (int i = 0; i < QR; i += 8) {
+                float4 x[2][4];
 #pragma unroll
-                for (int k = 0; k < 4; k++) v[k] = (float)(int8_t)(code >> (8 * k)) * qs;
-                const uint2 hi = make_uint2(f2_to_h2(v[0], v[1]), f2_to_h2(v[2], v[3]));
-                uint8_t* o = sm + Sh::Q + tile * TC_OP + (lane >> 4) * TC_PANEL + r * 128 +
-                             ((((lane & 15) >> 1) ^ (r & 7)) << 4) + (lane & 1) * 8;
-                *reinterpret_cast<uint2*>(o) = hi;
-                if (HILO) {
-                    const float2 a = h2_to_f2(hi.x), b = h2_to_f2(hi.y);
-                    *reinterpret_cast<uint2*>(o + TC_OP) =
-                        make_uint2(f2_to_h2(v[0] - a.x, v[1] - a.y), f2_to_h2(v[2] - b.x, v[3] - b.y));
+                for (int u = 0; u < 2; u++) {
+                    const int r = (SPLIT ? 64 * t : 0) + w4 * QR + i + 4 * u + (lane >> 3);
+                    const unsigned rr = (unsigned)(r0 + r), nd = rr / (unsigned)P.G;
+                    const int64_t at = (int64_t)(it.s.q0 + (int)nd) * P.q_st +
+                                       (int64_t)(it.h * P.G + (int)(rr - nd * P.G)) * P.q_sh +
+                                       16 * (lane & 7);
+#pragma unroll
+                    for (int k = 0; k < 4; k++)
+                        x[u][k] = r < rows ? load_q4(P.q, HILO ? P.dtype : (int)KQ8_BF16, at + 4 * k)
+                                           : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                }
+#pragma unroll
+                for (int u = 0; u < 2; u++) {
+                    const int r = (SPLIT ? 64 * t : 0) + w4 * QR + i + 4 * u + (lane >> 3);
+                    float v[16];
+#pragma unroll
+                    for (int k = 0; k < 4; k++) {
+                        v[4 * k] = x[u][k].x;
+                        v[4 * k + 1] = x[u][k].y;
+                        v[4 * k + 2] = x[u][k].z;
+                        v[4 * k + 3] = x[u][k].w;
+                    }
+                    float m = 0.0f;
+#pragma unroll
+                    for (int k = 0; k < 16; k++) m = fmaxf(m, fabsf(v[k]));
+                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                    if (m < 1e-6f) m = 1.0f;
+                    const float iq = __fdiv_rn(127.0f, m);
+                    const float qs = __fmul_rn(m, inv127());
+                    float top = qs;
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                    // 127 * top in [2^13, 2^14) after the scale
+                    const int e = min(max((int)(__float_as_uint(top) >> 23) - 127 + 7 - 13, -100), 100);
+                    if ((lane & 7) == 0) rf_sm[128 * tile + r] = pow2i(e);
+                    const float f = qs * pow2i(-e);
+                    uint32_t hi[8], lo[8];
+#pragma unroll
+                    for (int k = 0; k < 8; k++) {
+                        float y[2];
+#pragma unroll
+                        for (int d = 0; d < 2; d++) {
+                            const float c = fminf(fmaxf(__fmul_rn(v[2 * k + d], iq), -128.0f), 127.0f);
+                            y[d] = truncf(c) * f;
+                        }
+                        hi[k] = f2_to_h2(y[0], y[1]);
+                        if (HILO) {
+                            const float2 h = h2_to_f2(hi[k]);
+                            lo[k] = f2_to_h2(y[0] - h.x, y[1] - h.y);
+                        }
+                    }
+                    uint8_t* o = sm + Sh::Q + tile * TC_OP + ((lane >> 2) & 1) * TC_PANEL + r * 128;
+                    const int c0 = ((2 * (lane & 3)) ^ (r & 7)) << 4, c1 = ((2 * (lane & 3) + 1) ^ (r & 7)) << 4;
+                    *reinterpret_cast<uint4*>(o + c0) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4*>(o + c1) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
+                    if (HILO) {
+                        *reinterpret_cast<uint4*>(o + TC_OP + c0) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        *reinterpret_cast<uint4*>(o + TC_OP + c1) = make_uint4(lo[4], lo[5], lo[6], lo[7]);
+                    }
                 }
             }
             tc::fence_smem_to_async();
@@ -593,14 +641,12 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                 if (SPLIT && (int)(g & 1) != t) continue;
                 const float* km = sc + (g & 3) * 384;
                 ok = all(wait(Sh::B_SCF + (g & 3), (g >> 2) & 1));
-                const uint32_t sn = HILO ? n >> 1 : n;
-                ok = ok && all(wait(Sh::B_SF + (HILO ? n & 1 : t), sn & 1));
+                ok = ok && all(wait(Sh::B_SF + t, n & 1));
                 if (!ok) break;
                 tc::fence_after_sync();
                 const int tile0 = 4 * (it.step0 + j);  // the step's first sub-tile
                 const float4* mt = meta + (g & 3) * 4;
                 const bool masked = (tile0 + 4) * TILE > it.s.base || mt[0].x + mt[1].x + mt[2].x + mt[3].x != 0.0f;
-                const uint32_t tS = col_s(t, n) + lanes;
                 bool lost = false;  // the row sees a V step that is not finite
                 // columns 32 w .. + 31: x * f is the score (base 2), -inf where the row does not
                 // see the token; top bounds the exponents of the V steps that it sees
@@ -653,11 +699,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                     far = fmaxf(far, fmaf(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), f, top));
                 }
                 const bool need = far > M + TC_TOP;
-                // PV of this stream's step before is in O (and, hi and lo, has read P)
-                if (!first) {
-                    if (!(ok = all(wait(Sh::B_PV + t, (n - 1) & 1)))) break;
-                    tc::fence_after_sync();
-                }
+                // (PV of the stream's step before is in O: S went over its weights.)
+                tc::fence_after_sync();
                 if (__any_sync(0xffffffffu, need)) {
                     const float m = need ? far - TC_AIM : M;
                     const float f = tr_ex2(M - m);
@@ -705,15 +748,12 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                         }
                     }
                     sum = fmaf(s2.x + s2.y, pow2i(-(int)ve), sum);
-                    tc::tmem_st16(tP + 16 * w, hi);
-                    if (HILO) tc::tmem_st16(tP + 64 + 16 * w, lo);
+                    tc::tmem_st16(tS + off_p(2 * w), hi);
+                    if (HILO) tc::tmem_st16(tS + off_p(2 * w) + 16, lo);
                     if (w & 1) {  // half of the weights, of which the product may begin
                         tc::fence_before_sync();
                         __syncwarp();
-                        if (lane == 0) {
-                            if (HILO && w == 3) tc_arrive(bars + Sh::B_SR + (n & 1));
-                            tc_arrive(bars + Sh::B_P + 2 * t + (w >> 1));
-                        }
+                        if (lane == 0) tc_arrive(bars + Sh::B_P + 2 * t + (w >> 1));
                     }
                 }
                 if (lost) sum = NAN;
