@@ -404,7 +404,9 @@ int kq8_decode_attn_q4(float* out, const float* q, const kq8_cache_t* cache,
  *                  values bit for bit.
  *   kq8_read_kv  : the values the rows stand for, code * (stored max * (1/127))
  *                  (q4: 1/7) as one fp32 product, rounded once to dtype.  The rows
- *                  stored must not overlap (KQ8_ERR_INVALID_ARG).
+ *                  stored must not overlap (KQ8_ERR_INVALID_ARG): not those of k, not
+ *                  those of v, nor one of k with one of v (where the two lie among
+ *                  each other they have the same strides).
  *   dtype  : KQ8_F32, KQ8_F16 or KQ8_BF16, of k and v both; pointers aligned to
  *            an element (rows whose base and strides are multiples of 8
  *            elements are copied 8 elements at a time).
@@ -432,11 +434,15 @@ int kq8_read_kv(const kq8_cache_t* cache, int32_t bits, void* k, void* v, int32_
  * those tokens (the same Q quantisation, scores and softmax), to fp32 rounding.
  *   out, q      : dtype [total_q][nq][128], packed by sequence; q with strides of
  *                 its tokens and heads in elements (multiples of 4), out
- *                 contiguous; both aligned to 4 elements.  Rows outside every
- *                 sequence stay as they were.
+ *                 contiguous; both aligned to 4 elements; out does not overlap q
+ *                 (KQ8_ERR_INVALID_ARG).  Rows outside every sequence stay as they
+ *                 were.
  *   dtype       : KQ8_F32, KQ8_F16 or KQ8_BF16, of q and out; outputs are rounded
- *                 once.  For bf16 the softmax weights enter the value product as
- *                 fp16 (11 bits), for the others as fp16 hi + lo (22 bits).
+ *                 once.  fp32 and fp16 outputs take Q's codes, K's and V's exactly or at
+ *                 22 bits and the softmax weights as fp16 hi + lo (22 bits).  bf16
+ *                 outputs, of 8 bits themselves, take the weights as fp16 (11 bits)
+ *                 and, where a sequence may have more than 32 rows (max_q_len * G),
+ *                 Q, K and V with their scales as fp16 too.
  *   tree_mask   : uint32 [total_q][mask_words]; bit j % 32 of word j / 32 of a node's
  *                 row: it attends node j (its own bit included).  mask_words * 32 >=
  *                 max_q_len; bits at and past nb_b are ignored.  A node that attends
@@ -447,7 +453,8 @@ int kq8_read_kv(const kq8_cache_t* cache, int32_t bits, void* k, void* v, int32_
  *   nq          : nq % nkv == 0, G = nq / nkv in 1..8.
  *   workspace   : kq8_tree_workspace_bytes(...) bytes, 256-byte aligned,
  *                 initialised once by kq8_workspace_init; calls that share it must
- *                 not overlap on the GPU.
+ *                 not overlap on the GPU.  After a call that set
+ *                 KQ8_STATUS_TIMEOUT it is initialised again.
  * Bad sequences and pages as kq8_prefill_attn.
  */
 #define KQ8_TREE_MAX_NODES 1024
@@ -488,7 +495,8 @@ int kq8_tree_commit(const kq8_cache_t* cache, int32_t bits, const int32_t* page_
  * prompt's first pass: no cache is read, so nothing is quantised):
  *   out[i][h] = sum_j softmax_j(scale * q[i][h] . k[j][h / G]) * v[j][h / G]
  * over the tokens j <= i of i's own sequence.
- *   out         : dtype [total][nq][128] (device), contiguous, 16-byte aligned.
+ *   out         : dtype [total][nq][128] (device), contiguous, 16-byte aligned; does
+ *                 not overlap q, k or v (KQ8_ERR_INVALID_ARG).
  *   q           : dtype [total][nq][128] with strides of its tokens and heads in
  *                 elements, k and v likewise [total][nkv][128]; the 128 elements of a
  *                 row adjacent, pointers 16-byte aligned, strides multiples of 8.

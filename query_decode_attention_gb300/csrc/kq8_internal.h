@@ -8,6 +8,7 @@
 #include <cuda_runtime.h>
 
 #include "kq8.h"
+#include "kq8_common.cuh"
 
 namespace kq8 {
 
@@ -18,6 +19,15 @@ struct PrefillParams;
 // Largest element stride a call takes (a token or head index times it stays
 // inside 64 bits).
 constexpr size_t MAX_STRIDE = (size_t)1 << 31;
+// Bytes from the first to the last element of n1 x n2 rows of HD elements at strides s1
+// and s2 (in elements, below MAX_STRIDE), and whether two stretches of memory meet.
+inline size_t rows_bytes(size_t n1, size_t s1, size_t n2, size_t s2, size_t element) {
+    return n1 && n2 ? ((n1 - 1) * s1 + (n2 - 1) * s2 + HD) * element : 0;
+}
+inline bool stretches_meet(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
+    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+    return a_bytes && b_bytes && (x < y ? y - x < a_bytes : x - y < b_bytes);
+}
 
 // kq8_write_kv / kq8_read_kv: rows of K and V outside the cache (element
 // strides, elements of a row adjacent) and the slot of each token.

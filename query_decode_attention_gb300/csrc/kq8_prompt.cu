@@ -446,6 +446,12 @@ extern "C" int kq8_prompt_attn(void* out, const void* q, const void* k, const vo
         if (x % 8 || x > MAX_STRIDE) return KQ8_ERR_INVALID_ARG;
     if ((uintptr_t)out % 16 || (uintptr_t)q % 16 || (uintptr_t)k % 16 || (uintptr_t)v % 16)
         return KQ8_ERR_INVALID_ARG;
+    // the inputs are read while other rows are written
+    const size_t out_bytes = rows_bytes(total, (size_t)nq * HD, nq, HD, 2);
+    if (stretches_meet(out, out_bytes, q, rows_bytes(total, st[0], nq, st[1], 2)) ||
+        stretches_meet(out, out_bytes, k, rows_bytes(total, st[2], nkv, st[3], 2)) ||
+        stretches_meet(out, out_bytes, v, rows_bytes(total, st[4], nkv, st[5], 2)))
+        return KQ8_ERR_INVALID_ARG;
     const bool bf16 = dtype == KQ8_BF16;
     const int G = nq / nkv, TQ = PR_ROWS / G;
     PromptParams p;

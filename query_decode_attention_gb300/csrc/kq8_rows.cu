@@ -457,11 +457,29 @@ bool rows_apart(int64_t s1, int64_t n1, int64_t s2, int64_t n2) {
     return s1 >= HD && s2 >= (n1 - 1) * s1 + HD;
 }
 
+// Whether two sets of such rows (each apart in itself) that lie `d` >= 0 elements from
+// each other are apart too: a row of one meets a row of the other only if d is within
+// HD of a difference i * s1 + j * s2, |i| < n1, |j| < n2, and of those only the nearest
+// ones can be.
+bool rows_interleave(int64_t d, int64_t s1, int64_t n1, int64_t s2, int64_t n2) {
+    if (n1 <= 1) s1 = 0;
+    if (n2 <= 1) s2 = 0;
+    if (s1 < s2) return rows_interleave(d, s2, n2, s1, n1);
+    const int64_t i0 = s1 ? d / s1 : 0;
+    for (int64_t i = i0; i <= i0 + 1 && i < n1; i++) {
+        const int64_t r = d > i * s1 ? d - i * s1 : i * s1 - d, j0 = s2 ? r / s2 : 0;
+        for (int64_t j = j0; j <= j0 + 1 && j < n2; j++)
+            if ((r > j * s2 ? r - j * s2 : j * s2 - r) < HD) return false;
+    }
+    return true;
+}
+
 // Checks, the choice of vector accesses (bases and strides multiples of 8
 // elements), launch.
 template <bool WRITE>
 int rows_impl(const kq8_cache_t* cache, int32_t bits, void* k, void* v, int32_t dtype,
-              size_t k_st, size_t k_sh, size_t v_st, size_t v_sh, const int32_t* slot, int32_t T, uint32_t* status, kq8_stream_t stream) {
+              size_t k_st, size_t k_sh, size_t v_st, size_t v_sh, const int32_t* slot, int32_t T,
+              uint32_t* status, kq8_stream_t stream) {
     int rc = check_cache_args(cache);
     if (rc) return rc;
     if (bits != 8 && bits != 4) return KQ8_ERR_UNSUPPORTED;
@@ -482,9 +500,19 @@ int rows_impl(const kq8_cache_t* cache, int32_t bits, void* k, void* v, int32_t 
     }
     // the rows a read stores must not overlap
     const int64_t heads = cache->num_kv_heads;
-    if (!WRITE && (!rows_apart((int64_t)k_st, T, (int64_t)k_sh, heads) ||
-                   !rows_apart((int64_t)v_st, T, (int64_t)v_sh, heads)))
-        return KQ8_ERR_INVALID_ARG;
+    if (!WRITE) {
+        if (!rows_apart((int64_t)k_st, T, (int64_t)k_sh, heads) ||
+            !rows_apart((int64_t)v_st, T, (int64_t)v_sh, heads))
+            return KQ8_ERR_INVALID_ARG;
+        if (stretches_meet(k, rows_bytes(T, k_st, heads, k_sh, es), v,
+                           rows_bytes(T, v_st, heads, v_sh, es))) {
+            const bool same = (T == 1 || k_st == v_st) && (heads == 1 || k_sh == v_sh);
+            const uintptr_t x = (uintptr_t)k, y = (uintptr_t)v;
+            if (!same || !rows_interleave((int64_t)((x < y ? y - x : x - y) / es), (int64_t)k_st, T,
+                                          (int64_t)k_sh, heads))
+                return KQ8_ERR_INVALID_ARG;
+        }
+    }
     RowsParams p;
     p.cache = *cache;
     p.k = k;

@@ -652,6 +652,10 @@ int kq8_tree_attn(void* out, const void* q, int32_t dtype, size_t q_token_stride
         q_token_stride > MAX_STRIDE || q_head_stride > MAX_STRIDE ||
         (tree_mask && (uintptr_t)tree_mask % 4))
         return KQ8_ERR_INVALID_ARG;
+    // q is read while other rows are written
+    if (stretches_meet(out, rows_bytes(total_q, (size_t)nq * HD, nq, HD, quad / 4), q,
+                       rows_bytes(total_q, q_token_stride, nq, q_head_stride, quad / 4)))
+        return KQ8_ERR_INVALID_ARG;
     TreeParams p;
     std::memset(&p, 0, sizeof(p));
     rc = encode_vmap(&p.vmap, *cache, false);

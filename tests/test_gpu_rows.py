@@ -159,6 +159,52 @@ def test_skipped_and_bad_slots_leave_rows_alone():
     assert _same(cache, ref)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("bits", [8, 4])
+def test_a_bulk_call_equals_its_pieces(dtype, bits):
+    """Enough blocks for a bulk read's two sub-tiles a block (16 a multiprocessor), an odd
+    number of tokens, skipped slots in between and bad ones at the end."""
+    nkv = 8
+    T = torch.cuda.get_device_properties(0).multi_processor_count * 16 * 32 // nkv + 45
+    pages = -(-T // 64) + 1
+    a, b = _filled(pages, nkv, 64, bits), _filled(pages, nkv, 64, bits)
+    slots = np.random.default_rng(5).permutation(pages * 64)[:T].astype(np.int32)
+    slots[7::97] = -1
+    slots[-1] = pages * 64
+    st = torch.tensor(slots, device=DEV)
+    k, v = (_strided((T, nkv, 128), dtype, "packed", s) for s in (1, 2))
+    status = torch.zeros(2, dtype=torch.int32, device=DEV)
+    kq8.kq8_write_kv(a, k, v, st, status[:1])
+    outs = [torch.full((T, nkv, 128), 77.0, dtype=dtype, device=DEV) for _ in range(4)]
+    kq8.kq8_read_kv(a, outs[0], outs[1], st, status[1:])
+    assert status.tolist() == [kq8.KQ8_STATUS_BAD_SLOT] * 2
+    for i in range(0, T, 1000):
+        kq8.kq8_write_kv(b, k[i:i + 1000], v[i:i + 1000], st[i:i + 1000])
+        kq8.kq8_read_kv(b, outs[2][i:i + 1000], outs[3][i:i + 1000], st[i:i + 1000])
+    assert _same(a, b)
+    assert torch.equal(outs[0], outs[2]) and torch.equal(outs[1], outs[3])
+    assert bool((outs[0][7::97] == 77).all()) and bool((outs[0][-1] == 77).all())
+
+
+@pytest.mark.parametrize("shape", ["token", "head"])
+def test_read_into_rows_among_each_other(shape):
+    """K and V rows interleaved by token ([T, 2, nkv, 128]) or by head ([T, nkv, 2, 128])."""
+    T, nkv = 70, 3
+    cache = _filled(4, nkv, 32, 8)
+    slot = torch.arange(T, dtype=torch.int32, device=DEV) + 9
+    want = [torch.empty((T, nkv, 128), dtype=torch.float16, device=DEV) for _ in range(2)]
+    kq8.kq8_read_kv(cache, *want, slot)
+    both = torch.zeros((T, 2, nkv, 128) if shape == "token" else (T, nkv, 2, 128),
+                       dtype=torch.float16, device=DEV)
+    k, v = both.unbind(1 if shape == "token" else 2)
+    for x, y in ((k, v), (v, k)):
+        both.zero_()
+        kq8.kq8_read_kv(cache, x, y, slot)
+        assert torch.equal(x, want[0]) and torch.equal(y, want[1])
+    with pytest.raises(kq8.Kq8Error):
+        kq8.kq8_read_kv(cache, k, k, slot)
+
+
 def test_no_tokens():
     cache = _filled(2, 2, 32, 8)
     before = _clone(cache)

@@ -349,3 +349,41 @@ def test_two_streams_with_their_own_workspaces_and_a_graph():
                 g.replay()
     torch.cuda.synchronize()
     assert torch.equal(a.out, want[0]) and torch.equal(b.out, want[1])
+
+
+def test_all_forms_share_a_workspace_and_replay():
+    """One and two 16-row tiles a warp, one and two 128-row tiles, hi and lo parts: each
+    captured, then replayed in turn over one workspace, with other queries at the second
+    time."""
+    cases = [Case(4, 2, [3000, 100], [5, 3], torch.float32, seed=31),
+             Case(8, 2, [2500], [7], torch.bfloat16, seed=32),
+             Case(8, 2, [4000, 77, 900], [20, 9, 32], torch.bfloat16, seed=33),
+             Case(16, 2, [1500, 2100], [31, 17], torch.bfloat16, seed=34),
+             Case(8, 2, [2222, 640], [40, 11], torch.float32, seed=35)]
+    size = max(kq8.kq8_tree_workspace_bytes(len(c.lens), c.nq, 2, max(c.lens), max(c.nodes))
+               for c in cases)
+    ws = kq8.new_workspace(size, DEV)
+    s = torch.cuda.Stream()
+    graphs = []
+    with torch.cuda.stream(s):
+        for c in cases:
+            args = (_ints(c.table), _ints(c.lens), _ints(c.off), c.mask(), max(c.lens), max(c.nodes))
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=s):
+                kq8.kq8_tree_attn(c.out, c.q, c.cache, *args, SCALE, ws)
+            graphs.append((g, args))
+        for turn in range(2):
+            for c, (g, _) in zip(cases, graphs):
+                g.replay()
+            assert kq8.kq8_read_status(ws) == 0
+            for c in cases:
+                c.check(*c.reference())
+                c.q.copy_(c.q.flip(0))
+    torch.cuda.synchronize()
+
+
+def test_out_over_q_is_refused():
+    c = Case(8, 2, [100], [4], torch.bfloat16, layout="packed", seed=36)
+    c.out = c.q
+    with pytest.raises(kq8.Kq8Error):
+        c.run()

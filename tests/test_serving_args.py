@@ -55,8 +55,21 @@ def test_a_read_refuses_overlapping_rows(lib):
         assert _rows(fn, lib, st=st) == bad, st
 
 
+def test_a_read_refuses_k_rows_over_v_rows(lib):
+    """k and v of 4 tokens x 8 heads: the same rows, rows that touch, and rows that lie
+    among each other with other strides.  (What is apart is read on the GPU.)"""
+    fn, bad = lib._lib.kq8_read_kv, lib.KQ8_ERR_INVALID_ARG
+    k = 1 << 20
+    for d, st in ((0, (1024, 128)), (64, (1024, 128)), (1024 * 3, (1024, 128)),
+                  (1024 * 3 + 127, (1024, 128)), (256, (4096, 256)), (127, (4096, 256)),
+                  (4096 * 3 + 256 * 7 + 127, (4096, 256)), (128, (128, 512)), (128 * 3, (128, 512))):
+        for a, b in ((k, k + 2 * d), (k + 2 * d, k)):
+            assert _rows(fn, lib, k=a, v=b, st=st + st) == bad, (d, st)
+    assert _rows(fn, lib, k=k, v=k + 2 * 128, st=(2048, 256, 2048, 128)) == bad
+
+
 def _tree(lib, cache=None, dtype=2, qs=(2048, 128), total_q=8, max_pages=2, mask=256, words=1,
-          max_seq_len=64, max_q_len=8, B=1, nq=16, ws=512, ws_bytes=1 << 30, out=256, q=256,
+          max_seq_len=64, max_q_len=8, B=1, nq=16, ws=512, ws_bytes=1 << 30, out=1 << 30, q=256,
           pt=256, sl=256, qo=256):
     return lib._lib.kq8_tree_attn(out, q, dtype, *qs, total_q, ctypes.byref(cache or _cache(lib)),
                                   pt, max_pages, sl, qo, mask, words, max_seq_len, max_q_len, B,
@@ -73,7 +86,8 @@ def test_tree_refusals(lib):
     for kw in (dict(B=-1), dict(total_q=-1), dict(max_q_len=-1), dict(words=-1),
                dict(max_seq_len=65), dict(max_q_len=33, words=2, max_seq_len=32),
                dict(max_q_len=33, words=1), dict(out=None), dict(q=None), dict(sl=None),
-               dict(qo=None), dict(pt=None), dict(q=260), dict(out=258), dict(q=264, dtype=0),
+               dict(qo=None), dict(pt=None), dict(q=260), dict(out=(1 << 30) + 2), dict(q=264, dtype=0),
+               dict(out=256), dict(out=256 + 2 * 8 * 2048 - 8), dict(q=(1 << 30) + 8),
                dict(qs=(2046, 128)), dict(qs=(2048, 130)), dict(qs=(1 << 40, 128)),
                dict(mask=258)):
         assert _tree(lib, **kw) == bad, kw
@@ -111,7 +125,7 @@ def test_commit_refusals(lib):
         assert _commit(lib, **kw) == bad, kw
 
 
-def _prompt(lib, out=256, q=256, k=256, v=256, dtype=2, st=(4096, 128) * 3, cu=256, total=64,
+def _prompt(lib, out=1 << 30, q=256, k=256, v=256, dtype=2, st=(4096, 128) * 3, cu=256, total=64,
             max_len=64, B=1, nq=16, nkv=8, scale=0.1, status=None):
     return lib._lib.kq8_prompt_attn(out, q, k, v, dtype, *st, cu, total, max_len, B, nq, nkv, scale,
                                     status, None)
@@ -127,7 +141,9 @@ def test_prompt_refusals(lib):
     for kw in (dict(B=-1), dict(total=-1), dict(max_len=-1), dict(nq=0), dict(nkv=0),
                dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")),
                dict(scale=float("inf")), dict(out=None), dict(q=None), dict(k=None), dict(v=None),
-               dict(cu=None), dict(out=264), dict(q=264), dict(k=258), dict(v=264),
+               dict(cu=None), dict(out=(1 << 30) + 8), dict(out=256),
+               dict(q=(1 << 30) + 2 * 2048 * 64 - 16), dict(k=(1 << 30) - 2 * 64 * 4096 + 8192),
+               dict(v=1 << 30), dict(q=264), dict(k=258), dict(v=264),
                dict(st=(4100, 128) * 3), dict(st=(4096, 128, 4096, 132, 4096, 128)),
                dict(st=(4096, 128, 4096, 128, 1 << 40, 128)), dict(status=257)):
         assert _prompt(lib, **kw) == bad, kw
