@@ -441,8 +441,8 @@ int kq8_read_kv(const kq8_cache_t* cache, int32_t bits, void* k, void* v, int32_
  *                 once.  fp32 and fp16 outputs take Q's codes, K's and V's exactly or at
  *                 22 bits and the softmax weights as fp16 hi + lo (22 bits).  bf16
  *                 outputs, of 8 bits themselves, take the weights as fp16 (11 bits)
- *                 and, where a sequence may have more than 32 rows (max_q_len * G),
- *                 Q, K and V with their scales as fp16 too.
+ *                 and, where max_q_len * G is above 32, Q and V with their scales as
+ *                 fp16 too, above 128 K as well.
  *   tree_mask   : uint32 [total_q][mask_words]; bit j % 32 of word j / 32 of a node's
  *                 row: it attends node j (its own bit included).  mask_words * 32 >=
  *                 max_q_len; bits at and past nb_b are ignored.  A node that attends

@@ -535,7 +535,7 @@ struct TreePlan {
     int tile_rows = 16;  // 16, 32: kq8_tree_kernel; 128, 256: the tensor cores
     int ctas = 0;        // of the tensor cores' kernel
     int seqs = 0, row_tiles = 1, chunk_tiles = TR_WARPS, num_chunks = 1;
-    size_t off_ms = 0, off_acc = 0, total = TR_HEADER;
+    size_t off_ms = 0, off_acc = 0, off_spill = 0, total = TR_HEADER;
 };
 constexpr int64_t TR_PARTS = 512ll << 20;  // bytes of partials a call may take
 
@@ -543,7 +543,7 @@ constexpr int64_t TR_PARTS = 512ll << 20;  // bytes of partials a call may take
 // tail): of the chunk counts that allow, the one whose waves of resident CTAs take
 // least, a CTA's prologue and merge costing TR_CTA_TILES sub-tiles of a warp beside its
 // walk.  Uniform lists of 512 sub-tiles, 128 of them, 32 rows: chunks of 56 in 4.2
-// waves 192 us, of 76 in 2.9 waves 160 us.
+// waves 192 us, of 76 in 2.9 waves 186 us.
 constexpr int64_t TR_CTA_TILES = 5;
 int64_t tree_chunk(int64_t pairs, int64_t tiles, int ctas_per_sm) {
     const int64_t slots = (int64_t)device_sms() * ctas_per_sm;
@@ -562,6 +562,11 @@ int64_t tree_chunk(int64_t pairs, int64_t tiles, int ctas_per_sm) {
     return best;
 }
 
+// Rows of a tile.  16 x 16384 tokens, 8 KV heads, bf16 (fp32): 16 rows take 104 (117) us
+// on one 16-row tile a warp; 32 rows 184 (216) on two, and on a tensor-core tile of 128
+// rows, which 32 rows fill as little as 64 do, 223 (350); two tiles of 32 rows take twice
+// 184, so from 33 rows on it is the tensor cores: 128 rows 231 (360), 256 rows 347 on a
+// pair of tiles that share K and V, two lists of one tile twice 231.
 TreePlan tree_plan(int B, int nq, int nkv, int max_seq_len, int max_q_len, bool hilo) {
     TreePlan p;
     const int64_t rows = (int64_t)max_q_len * (nq / nkv);
@@ -594,7 +599,8 @@ TreePlan tree_plan(int B, int nq, int nkv, int max_seq_len, int max_q_len, bool 
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     p.off_ms = TR_HEADER;
     p.off_acc = up(p.off_ms + parts * sizeof(float2));
-    p.total = up(p.off_acc + parts * HD * sizeof(float));
+    p.off_spill = up(p.off_acc + parts * HD * sizeof(float));
+    p.total = p.off_spill + (hilo ? (size_t)p.ctas * 2 * HD * 128 * sizeof(float) : 0);
     return p;
 }
 
@@ -684,6 +690,7 @@ int kq8_tree_attn(void* out, const void* q, int32_t dtype, size_t q_token_stride
     char* ws = static_cast<char*>(workspace);
     p.part_ms = reinterpret_cast<float2*>(ws + plan.off_ms);
     p.part_acc = reinterpret_cast<float*>(ws + plan.off_acc);
+    p.spill = reinterpret_cast<float*>(ws + plan.off_spill);
     p.status = reinterpret_cast<uint32_t*>(ws);
     p.counters = reinterpret_cast<uint32_t*>(ws + TR_STATUS_BYTES);
     const cudaStream_t st = (cudaStream_t)stream;

@@ -32,7 +32,8 @@ struct TreeParams {
     int32_t nq, G;
     float scale;
     int32_t chunk_tiles, num_chunks, row_tiles;
-    float* part_acc;       // [pairs][tile's rows][num_chunks][HD]; tensor cores: [CTA][2][rows][HD]
+    float* part_acc;
+    float* spill;          // tensor cores, hi and lo parts: [CTA][2][HD][128]
     float2* part_ms;       // the same places, without HD
     uint32_t* status;      // [0] status bits, [1] set by a CTA that gave up
     uint32_t* counters;    // [pairs]

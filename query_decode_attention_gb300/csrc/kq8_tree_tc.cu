@@ -8,22 +8,29 @@
 // per row that puts the row's largest near 2^13.  Outputs of 24 and 11 bits take K's and
 // V's codes as they are (exact in fp16), the tokens' scales in fp32 beside the softmax,
 // and Q and the weights p * vstep as fp16 hi and lo parts (22 bits), each an MMA of its
-// own.  bf16 outputs, whose own rounding is 2^-9, take Q and P at 11 bits, and K and V
-// already multiplied by their token's scale (relative to a power of two per 32 tokens),
-// 11 bits too: that leaves the softmax one multiply-add and one exponential per score
-// instead of two loads and three operations (128 rows of 16 x 16384 tokens: 350 us with
-// the scales beside the softmax, 296 with them in the operands).
+// own.  bf16 outputs, whose own rounding is 2^-9, take Q and P at 11 bits, V already
+// multiplied by its token's step (relative to a power of two per 32 tokens), 11 bits too,
+// and with two tiles K as well (KCODES): each multiplier in an operand spares the softmax
+// a load and an operation per score.
 //
 // What bounds it.  Per 128-token step shared memory carries the raw bytes in and out of
 // the ring (66 KB), the widened operands in (64 KB) and, per tile, Q and K (64 KB) and V
 // (32 KB) to the MMAs: 226 KB for one tile, 322 KB for two or for hi and lo, 1770 and
 // 2520 cycles at 128 bytes; the MMAs themselves take 1024 and 2048 (64 each), HBM 1440
 // for the step's 33 KB.  Measured, 16 x 16384 tokens, 8 KV heads (83 us of HBM): 128
-// rows bf16 221 us, 256 rows 342, 128 rows fp32 326: 3900, 6000 and 5700 cycles a step.
+// rows bf16 231 us, 256 rows 347, 128 rows fp32 360: 4100, 6100 and 6300 cycles a step.
 // The schedulers issue in half of the cycles; what is left is the latency of the chain
-// widen K -> S -> widen K and of the roles' own code (steps of 64 tokens and K's and V's
-// raw bytes in rings of their own, which loosen the chain, gained nothing: 390 and 226
-// us at 128 rows).  With few rows the mma.sync kernel moves less: see tree_plan.
+// widen K -> S -> widen K and of the roles' own code.  Tried at 128 rows and dropped, as
+// they loosen the chain and gain nothing: steps of 64 tokens (390 against 296 us), K's and
+// V's raw bytes in rings of their own (226 against 221), second places of both K and V
+// (275 to 291).  With few rows the mma.sync kernel moves less: see tree_plan.
+//
+// Sums.  The tensor core adds products to its fp32 accumulator by cutting off, so a long
+// chain of steps drifts: 1.3e-5 of the output (2-norm) after 47 steps of a stream, where
+// plain fp32 sums are off by 6e-6.  fp32 and fp16 outputs therefore take O out of the
+// accumulator every TC_FLUSH steps and add it to a sum in memory (L2), rounded to nearest:
+// 5.8e-6, for a tenth of the time (128 rows 326 -> 360 us).  For bf16 outputs the drift
+// is a hundredth of their own rounding.
 //
 // One persistent CTA per SM takes an equal share of all steps: the lists (row tile, KV
 // head, sequence) lie one behind the other and are cut where a share ends, so ragged
@@ -66,6 +73,8 @@ constexpr int TC_REGS_SOFTMAX = 136, TC_REGS_WIDEN = 64, TC_REGS_REST = 80;
 constexpr uint32_t TC_PANEL = TC_STEP * 128;     // 128 rows x 64 fp16
 constexpr uint32_t TC_OP = 2 * TC_PANEL;         // an operand: 128 rows x 128 fp16
 constexpr float TC_M_INIT = -1e30f;              // reference of a row that saw nothing
+// hi and lo parts: O leaves the accumulator after so many steps of a stream
+constexpr int TC_FLUSH = 16;
 constexpr float TC_TOP = 15.0f, TC_AIM = 7.0f;   // weights stay below 2^15, are set to 2^7
 
 template <int T, bool HILO>
@@ -76,14 +85,14 @@ struct TcShape {
     // that waits for every phase of a barrier, in order: so the raw ring is a multiple
     // of four long (a place has the same two consumers, sub-tile w's K and V warp).
     // One tile and one part leave room for a second place of K or of V; V's it is:
-    // 128 rows of 16 x 16384 tokens take 268 us so, 292 with K's.  Raw places given up
+    // 128 rows of 16 x 16384 tokens took 268 us so, 292 with K's.  Raw places given up
     // for either cost more than it gains.
     static constexpr int RAWN = 8, KB = 1, VB = T == 1 && !HILO ? 2 : 1;
     static constexpr uint32_t Q = 0, K = (T + (HILO ? 1 : 0)) * TC_OP, V = K + KB * TC_OP,
                               RAW = V + VB * TC_OP,
                               SC = RAW + RAWN * STAGE_BYTES,  // [4][3][128] floats
                               // [4][4]: something is missing or not finite, a bound of log2
-                              // of the V steps, K's factor, V's exponent
+                              // of the V steps, K's factor
                               META = SC + 4 * 3 * 512,
                               RF = META + 4 * 4 * 16,         // [T][128] row factors
                               EX = RF + T * 512,              // [2][128] (m, sum)
@@ -102,15 +111,22 @@ struct TcShape {
 
 __device__ __forceinline__ int tc_rho(int r) { return (r & ~6) | ((r & 2) << 1) | ((r & 4) >> 1); }
 
-// 8 int8 codes -> 8 fp16: exactly, or times an fp16 pair of equals.
-template <bool EXACT>
-__device__ __forceinline__ uint4 widen8(uint32_t a, uint32_t b, uint32_t f) {
+// 8 int8 codes -> 8 fp16: exactly, or times f (an fp16 pair of equals), or times f + fl
+// with one rounding.  The last is K's: a token's factor of 11 bits would move all its
+// scores by 2^-12 of themselves, which the rounding of 128 products does not.
+template <bool EXACT, bool LOW = false>
+__device__ __forceinline__ uint4 widen8(uint32_t a, uint32_t b, uint32_t f, uint32_t fl = 0u) {
     const uint32_t u = a ^ 0x80808080u, v = b ^ 0x80808080u;
     auto half = [&](uint32_t w, uint32_t sel) {
         const uint32_t x = hsub2(__byte_perm(w, 0x64646464u, sel), 0x64806480u);
         if (EXACT) return x;
         uint32_t r;
-        asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(f));
+        if (LOW) {
+            asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(fl));
+            asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(r) : "r"(x), "r"(f));
+        } else {
+            asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(f));
+        }
         return r;
     };
     return make_uint4(half(u, 0x4140), half(u, 0x4342), half(v, 0x4140), half(v, 0x4342));
@@ -225,6 +241,10 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     kq8_tree_tc_kernel(const __grid_constant__ TreeParams P) {
     using Sh = TcShape<T, HILO>;
     constexpr int NR = Sh::NR, RAWN = Sh::RAWN, KB = Sh::KB, VB = Sh::VB;
+    // K's operand is its codes, with the tokens' multipliers beside the softmax, or their
+    // product.  With one tile a step waits for the widening, with two for the softmax
+    // (128 rows 231 and 256 us, 256 rows 387 and 347).
+    constexpr bool KCODES = T == 1;
     constexpr bool SPLIT = T == 1;  // the streams are the even and the odd steps
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -409,7 +429,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                 for (int j = 0; ok && j < it.steps; j++, g++) {
                     const int place = g % VB, t = SPLIT ? (int)(g & 1) : tile;
                     const uint32_t m = SPLIT ? g >> 1 : g;  // of the stream
-                    const bool first = j < (SPLIT ? 2 : 1);
+                    const bool first = HILO ? (j >> 1) % TC_FLUSH == 0 : j < (SPLIT ? 2 : 1);
                     const uint64_t v = dv + (uint64_t)(place * (TC_OP >> 4));
                     ok = wait(Sh::B_VF + place, (g / VB) & 1);
 #pragma unroll
@@ -478,13 +498,17 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                     d[256] = have ? lv : -INFINITY;                   // a missing page's: masked
                     if (lane == 0)
                         meta[(g & 3) * 4 + w] = make_float4(odd ? 1.0f : 0.0f, (float)ve,
-                                                            HILO ? 1.0f : pow2i(ke), 0.0f);
+                                                            KCODES ? 1.0f : pow2i(ke), 0.0f);
                     // K: lane = (position pair, 16-byte half); its 16 codes are chunks c, c + 1
                     // of the row's panel
-                    const uint32_t f = make_half2_bits(km * pow2i(-ke));
+                    const float fk = km * pow2i(-ke);
+                    const uint32_t f = make_half2_bits(fk);
+                    const uint32_t fl = make_half2_bits(fk - h2_to_f2(f).x);
                     const int rowa = 32 * w + tc_rho(lane >> 1), x7 = rowa & 7;
                     const uint32_t fa = __shfl_sync(0xffffffffu, f, rowa & 31);
                     const uint32_t fb = __shfl_sync(0xffffffffu, f, (rowa + 16) & 31);
+                    const uint32_t fla = __shfl_sync(0xffffffffu, fl, rowa & 31);
+                    const uint32_t flb = __shfl_sync(0xffffffffu, fl, (rowa + 16) & 31);
                     uint4 xa = *reinterpret_cast<const uint4*>(st + 16 * lane);
                     uint4 xb = *reinterpret_cast<const uint4*>(st + 512 + 16 * lane);
 #pragma unroll 1
@@ -497,10 +521,10 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                         const int c = (blk & 1) * 4 + (lane & 1) * 2;
                         uint8_t* o = sm + Sh::K + place * TC_OP + (blk >> 1) * TC_PANEL + rowa * 128;
                         const int c0 = (c ^ x7) << 4, c1 = ((c + 1) ^ x7) << 4;
-                        *reinterpret_cast<uint4*>(o + c0) = widen8<HILO>(ya.x, ya.y, fa);
-                        *reinterpret_cast<uint4*>(o + c1) = widen8<HILO>(ya.z, ya.w, fa);
-                        *reinterpret_cast<uint4*>(o + 2048 + c0) = widen8<HILO>(yb.x, yb.y, fb);
-                        *reinterpret_cast<uint4*>(o + 2048 + c1) = widen8<HILO>(yb.z, yb.w, fb);
+                        *reinterpret_cast<uint4*>(o + c0) = widen8<KCODES, true>(ya.x, ya.y, fa, fla);
+                        *reinterpret_cast<uint4*>(o + c1) = widen8<KCODES, true>(ya.z, ya.w, fa, fla);
+                        *reinterpret_cast<uint4*>(o + 2048 + c0) = widen8<KCODES, true>(yb.x, yb.y, fb, flb);
+                        *reinterpret_cast<uint4*>(o + 2048 + c1) = widen8<KCODES, true>(yb.z, yb.w, fb, flb);
                     }
                 } else {
                     if (g >= (uint32_t)VB && !(ok = all(wait(Sh::B_VE + place, (g / VB - 1) & 1)))) break;
@@ -551,6 +575,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         const uint32_t lanes = (uint32_t)(w4 * 32) << 16;
         const uint32_t tO = col_o(t) + lanes, tS = col_s(t) + lanes;
         float2* ex = reinterpret_cast<float2*>(sm + Sh::EX);
+        float* spill = HILO ? P.spill + ((size_t)blockIdx.x * 2 + t) * HD * 128 + row : nullptr;
         uint32_t g = 0, n = 0, xn = 0;  // steps, this stream's steps, lists so far
         bool ok = true;
         for (int piece = 0; ok && walk.next(P, NR, it); piece++) {
@@ -636,7 +661,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             const int node = (r0 + row) / P.G;
             float M = TC_M_INIT;
             float sum = 0.0f;
-            bool first = true;
+            bool first = true, spilled = false;
+            float M_spill = 0.0f;  // the reference of what has been spilled
             for (int j = 0; ok && j < it.steps; j++, g++) {
                 if (SPLIT && (int)(g & 1) != t) continue;
                 const float* km = sc + (g & 3) * 384;
@@ -655,7 +681,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                     const float4 m = mt[w];
                     f = rf * m.z;
                     top = m.y;
-                    if (HILO) {
+                    if (KCODES) {
 #pragma unroll
                         for (int c = 0; c < 32; c += 4) {
                             const float4 k4 = *reinterpret_cast<const float4*>(km + 32 * w + c);
@@ -700,7 +726,26 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                 }
                 const bool need = far > M + TC_TOP;
                 // (PV of the stream's step before is in O: S went over its weights.)
-                tc::fence_after_sync();
+                if (HILO && j >= 2 && (j >> 1) % TC_FLUSH == 0) {
+                    const float f = tr_ex2(M_spill - M);
+#pragma unroll 1
+                    for (int c = 0; c < HD / 32; c++) {
+                        float o[32], a[32];
+                        float* at = spill + 32 * c * 128;
+                        if (spilled) {
+#pragma unroll
+                            for (int i = 0; i < 32; i++) a[i] = __ldcg(at + 128 * i);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 32; i++) a[i] = 0.0f;
+                        }
+                        tc::tmem_ld32(tO + 32 * c, o);
+#pragma unroll
+                        for (int i = 0; i < 32; i++) __stcg(at + 128 * i, fmaf(a[i], f, o[i]));
+                    }
+                    M_spill = M;
+                    spilled = first = true;
+                }
                 if (__any_sync(0xffffffffu, need)) {
                     const float m = need ? far - TC_AIM : M;
                     const float f = tr_ex2(M - m);
@@ -764,15 +809,30 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                 if (!(ok = all(wait(Sh::B_PV + t, (n - 1) & 1)))) break;
                 tc::fence_after_sync();
             }
+            if (HILO && spilled) {
+                const float f = tr_ex2(M_spill - M);
+#pragma unroll 1
+                for (int c = 0; c < HD / 32; c++) {
+                    float o[32], a[32];
+#pragma unroll
+                    for (int i = 0; i < 32; i++) a[i] = __ldcg(spill + (32 * c + i) * 128);
+                    tc::tmem_ld32(tO + 32 * c, o);
+#pragma unroll
+                    for (int i = 0; i < 32; i++) o[i] = fmaf(a[i], f, o[i]);
+                    tc::tmem_st32(tO + 32 * c, o);
+                }
+            }
             // ---- the list's result.  The streams of one tile meet: each then writes half
             // of the dimensions from both O's.
             float den = sum;
             float f[2] = {1.0f, 0.0f};
             if (SPLIT) {
                 ex[128 * t + row] = make_float2(M, den);
+                tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) tc_arrive(bars + Sh::B_XF);
                 if (!(ok = all(wait(Sh::B_XF, xn & 1)))) break;
+                tc::fence_after_sync();
                 const float2 a = ex[row], b = ex[128 + row];
                 M = fmaxf(a.x, b.x);
                 f[0] = a.y == 0.0f ? 0.0f : tr_ex2(a.x - M);

@@ -351,6 +351,40 @@ def test_two_streams_with_their_own_workspaces_and_a_graph():
     assert torch.equal(a.out, want[0]) and torch.equal(b.out, want[1])
 
 
+def test_sums_that_leave_the_accumulator():
+    """Shares of 40 steps of 128 tokens: hi and lo parts take O out of the accumulator twice
+    on the way; a third of the tokens raises the reference late."""
+    nkv, B = 8, 2
+    n = torch.cuda.get_device_properties(0).multi_processor_count * 40 * 128 // (nkv * B) + 77
+    c = Case(16, nkv, [n, n - 500], [20, 18], torch.float32, seed=37)
+    late = torch.tensor(np.concatenate([s[2 * len(s) // 3:] for s in c.slots]), device=DEV)
+    k, v = (torch.empty((len(late), nkv, 128), device=DEV) for _ in range(2))
+    kq8.kq8_read_kv(c.cache, k, v, late.int())
+    kq8.kq8_write_kv(c.cache, 2 * k, v, late.int())
+    assert c.run() == 0
+    # the method in float64 on the GPU, one head at a time
+    ks, vs = (torch.empty((sum(c.lens), nkv, 128), device=DEV) for _ in range(2))
+    kq8.kq8_read_kv(c.cache, ks, vs, _ints(np.concatenate(c.slots)))
+    x = c.q.reshape(c.total, 16, 4, 32)
+    m = x.abs().amax(-1, keepdim=True)
+    code = torch.trunc((x * (torch.tensor(127.0, device=DEV) / m)).clamp(-128, 127)).double()
+    qd = (code * (m * (torch.tensor(1.0, device=DEV) / 127)).double()).reshape(c.total, 16, 128)
+    ref, at = torch.empty_like(qd), 0
+    for b, n in enumerate(c.lens):
+        nb, o = c.nodes[b], int(c.off[b])
+        see = torch.tensor(c.bits[o:o + nb, :nb], device=DEV)
+        for h in range(16):
+            kd, vd = ks[at:at + n, h // 2].double(), vs[at:at + n, h // 2].double()
+            s = qd[o:o + nb, h] @ kd.T * SCALE
+            s[:, n - nb:][~see] = -torch.inf
+            ref[o:o + nb, h] = torch.softmax(s, -1) @ vd
+        at += n
+    # a chain of 16 steps is 256 additions of half a last place, cut off: 256 * 2^-24 of the
+    # sums' size, which the later chains' own sums (rounded to nearest) hardly add to; the
+    # read rows are one rounding, 2^-24, off, scores with it
+    assert float((c.out.double() - ref).norm()) <= 2.0 ** -16 * float(ref.norm())
+
+
 def test_all_forms_share_a_workspace_and_replay():
     """One and two 16-row tiles a warp, one and two 128-row tiles, hi and lo parts: each
     captured, then replayed in turn over one workspace, with other queries at the second
