@@ -8,7 +8,9 @@
 // ((sum_b dot_b * qsc_b) * ks) * scale with exact integer block dots, a one-pass
 // softmax, one divide at the end.
 //
-// Work decomposition: CTA = (KV chunk, tile of 16 rows, KV head, sequence), 4
+// Up to 32 rows (nodes x query heads) of a KV head; more go to kq8_tree_tc.cu.
+//
+// Work decomposition: CTA = (KV chunk, tile of 16 or 32 rows, KV head, sequence), 4
 // warps.  The rows of a KV head are its G query heads of every node.  As in the
 // decode kernel each warp owns a two-stage ring of 32-token sub-tiles filled by
 // bulk and tensor copies, and takes every fourth sub-tile of its chunk; chunks
@@ -30,6 +32,10 @@
 // eight V rows of a transposed 8 x 8 load are tok(i, 0..7): all different
 // modulo 8, so the 128-byte swizzle keeps that load free of conflicts too.
 // The weights therefore go from accumulators to operands within the lane.
+// Measured, 16 x 16384 tokens, 8 KV heads (553 MB), bf16: 8 rows 101 us, 16 rows 104 us =
+// 5.3 TB/s, near what HBM gives (82 us) with 12 warps an SM and the waves of chunks; 32
+// rows 174 us = 3.2 TB/s, bound by latency: 8 warps an SM at 255 registers issue in a third
+// of the cycles.
 #include <cstring>
 #include <type_traits>
 
@@ -150,14 +156,25 @@ __global__ void __launch_bounds__(TR_THREADS, TreeShape<MT>::CTAS)
     for (int i = 0; i < TR_STAGES && i < mine; i++) issue(i);
 
     // ---- Q's codes while the first copies are in flight (article 9-2 §2 seg. 1)
-    for (int r = warp; r < TR_ROWS; r += TR_WARPS) {
-        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (r < rows) {
-            const int rr = rt * TR_ROWS + r, node = rr / G, hq = h * G + rr % G;
-            x = load_q4(P.q, P.dtype, (int64_t)(q0 + node) * P.q_st + hq * P.q_sh + 4 * lane);
+    // A warp's rows, their loads in flight together: a chunk pays this prologue before it
+    // can use its first tile.
+    constexpr int QROWS = TR_ROWS / TR_WARPS;
+    float4 qx[QROWS];
+    load_type<HILO>(P.dtype, [&](auto type) {
+#pragma unroll
+        for (int i = 0; i < QROWS; i++) {
+            const int r = warp + i * TR_WARPS, rr = rt * TR_ROWS + r, node = rr / G;
+            qx[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (r < rows)
+                qx[i] = load_q4(P.q, decltype(type)::value, (int64_t)(q0 + node) * P.q_st +
+                                                                (h * G + rr % G) * P.q_sh + 4 * lane);
         }
+    });
+#pragma unroll
+    for (int i = 0; i < QROWS; i++) {
+        const int r = warp + i * TR_WARPS;
         float qs;
-        const uint32_t u = quantize_q_lane(x, qs) ^ 0x80808080u;
+        const uint32_t u = quantize_q_lane(qx[i], qs) ^ 0x80808080u;
         // this lane's codes are elements 8c + 4s .. + 3 of block lane / 8, c = lane % 8 / 2,
         // s = lane % 2: registers half and half + 2 of k-step s for lane (row % 8, c)
         uint32_t* f = reinterpret_cast<uint32_t*>(
@@ -542,9 +559,10 @@ constexpr int64_t TR_PARTS = 512ll << 20;  // bytes of partials a call may take
 // Sub-tiles per chunk, at most TR_MAX_CHUNK (a long chunk of a ragged batch is a long
 // tail): of the chunk counts that allow, the one whose waves of resident CTAs take
 // least, a CTA's prologue and merge costing TR_CTA_TILES sub-tiles of a warp beside its
-// walk.  Uniform lists of 512 sub-tiles, 128 of them, 32 rows: chunks of 56 in 4.2
-// waves 192 us, of 76 in 2.9 waves 186 us.
-constexpr int64_t TR_CTA_TILES = 5;
+// walk.  Uniform lists of 512 sub-tiles, 128 of them, 32 rows: 184 us with a CTA's
+// cost put at 5 sub-tiles, 174 at 10; ragged lists of 1K to 32K tokens, 512 of them: chunks
+// of at most 64 sub-tiles 719 us, 96 695, 128 658, 192 657.
+constexpr int64_t TR_CTA_TILES = 10;
 int64_t tree_chunk(int64_t pairs, int64_t tiles, int ctas_per_sm) {
     const int64_t slots = (int64_t)device_sms() * ctas_per_sm;
     const int64_t least = (tiles + TR_MAX_CHUNK - 1) / TR_MAX_CHUNK;
@@ -562,11 +580,11 @@ int64_t tree_chunk(int64_t pairs, int64_t tiles, int ctas_per_sm) {
     return best;
 }
 
-// Rows of a tile.  16 x 16384 tokens, 8 KV heads, bf16 (fp32): 16 rows take 104 (117) us
-// on one 16-row tile a warp; 32 rows 184 (216) on two, and on a tensor-core tile of 128
-// rows, which 32 rows fill as little as 64 do, 223 (350); two tiles of 32 rows take twice
-// 184, so from 33 rows on it is the tensor cores: 128 rows 231 (360), 256 rows 347 on a
-// pair of tiles that share K and V, two lists of one tile twice 231.
+// Rows of a tile.  16 x 16384 tokens, 8 KV heads, bf16 (fp32): 16 rows take 104 (116) us
+// on one 16-row tile a warp; 32 rows 174 (210) on two, and on a tensor-core tile of 128
+// rows, which costs 64 rows as much, 226 (332); two tiles of 32 rows take twice 174, so
+// from 33 rows on it is the tensor cores: 128 rows 234 (339), 256 rows 340 on a pair of
+// tiles that share K and V, twice 234 as lists of one tile.
 TreePlan tree_plan(int B, int nq, int nkv, int max_seq_len, int max_q_len, bool hilo) {
     TreePlan p;
     const int64_t rows = (int64_t)max_q_len * (nq / nkv);

@@ -4,6 +4,8 @@
 
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "kq8_common.cuh"
 
 namespace kq8 {
@@ -55,6 +57,17 @@ __device__ __forceinline__ float4 load_q4(const void* q, int dtype, int64_t at) 
     }
     return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u),
                        __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u));
+}
+// load(type code as a constant) for the call's type: bf16, or with hi and lo parts fp32
+// or fp16.  A batch of loads behind one branch stays in flight together.
+template <bool HILO, typename F>
+__device__ __forceinline__ void load_type(int dtype, F&& load) {
+    if (!HILO)
+        load(std::integral_constant<int, KQ8_BF16>{});
+    else if (dtype == KQ8_F32)
+        load(std::integral_constant<int, KQ8_F32>{});
+    else
+        load(std::integral_constant<int, KQ8_F16>{});
 }
 // One rounding to the output type.
 __device__ __forceinline__ void store_out4(void* out, int dtype, size_t at, const float4 x) {

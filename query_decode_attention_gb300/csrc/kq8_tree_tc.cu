@@ -18,7 +18,7 @@
 // (32 KB) to the MMAs: 226 KB for one tile, 322 KB for two or for hi and lo, 1770 and
 // 2520 cycles at 128 bytes; the MMAs themselves take 1024 and 2048 (64 each), HBM 1440
 // for the step's 33 KB.  Measured, 16 x 16384 tokens, 8 KV heads (83 us of HBM): 128
-// rows bf16 231 us, 256 rows 347, 128 rows fp32 360: 4100, 6100 and 6300 cycles a step.
+// rows bf16 234 us, 256 rows 340, 128 rows fp32 339: 4100, 6000 and 6000 cycles a step.
 // The schedulers issue in half of the cycles; what is left is the latency of the chain
 // widen K -> S -> widen K and of the roles' own code.  Tried at 128 rows and dropped, as
 // they loosen the chain and gain nothing: steps of 64 tokens (390 against 296 us), K's and
@@ -29,7 +29,7 @@
 // chain of steps drifts: 1.3e-5 of the output (2-norm) after 47 steps of a stream, where
 // plain fp32 sums are off by 6e-6.  fp32 and fp16 outputs therefore take O out of the
 // accumulator every TC_FLUSH steps and add it to a sum in memory (L2), rounded to nearest:
-// 5.8e-6, for a tenth of the time (128 rows 326 -> 360 us).  For bf16 outputs the drift
+// 5.8e-6, for a tenth of the time (128 rows 326 -> 360 us when it came in).  For bf16 outputs the drift
 // is a hundredth of their own rounding.
 //
 // One persistent CTA per SM takes an equal share of all steps: the lists (row tile, KV
@@ -590,18 +590,20 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
 #pragma unroll 1
             for (int i = 0; i < QR; i += 8) {
                 float4 x[2][4];
+                load_type<HILO>(P.dtype, [&](auto type) {
 #pragma unroll
-                for (int u = 0; u < 2; u++) {
-                    const int r = (SPLIT ? 64 * t : 0) + w4 * QR + i + 4 * u + (lane >> 3);
-                    const unsigned rr = (unsigned)(r0 + r), nd = rr / (unsigned)P.G;
-                    const int64_t at = (int64_t)(it.s.q0 + (int)nd) * P.q_st +
-                                       (int64_t)(it.h * P.G + (int)(rr - nd * P.G)) * P.q_sh +
-                                       16 * (lane & 7);
+                    for (int u = 0; u < 2; u++) {
+                        const int r = (SPLIT ? 64 * t : 0) + w4 * QR + i + 4 * u + (lane >> 3);
+                        const unsigned rr = (unsigned)(r0 + r), nd = rr / (unsigned)P.G;
+                        const int64_t at = (int64_t)(it.s.q0 + (int)nd) * P.q_st +
+                                           (int64_t)(it.h * P.G + (int)(rr - nd * P.G)) * P.q_sh +
+                                           16 * (lane & 7);
 #pragma unroll
-                    for (int k = 0; k < 4; k++)
-                        x[u][k] = r < rows ? load_q4(P.q, HILO ? P.dtype : (int)KQ8_BF16, at + 4 * k)
-                                           : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                }
+                        for (int k = 0; k < 4; k++)
+                            x[u][k] = r < rows ? load_q4(P.q, decltype(type)::value, at + 4 * k)
+                                               : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    }
+                });
 #pragma unroll
                 for (int u = 0; u < 2; u++) {
                     const int r = (SPLIT ? 64 * t : 0) + w4 * QR + i + 4 * u + (lane >> 3);
@@ -666,13 +668,25 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             for (int j = 0; ok && j < it.steps; j++, g++) {
                 if (SPLIT && (int)(g & 1) != t) continue;
                 const float* km = sc + (g & 3) * 384;
-                ok = all(wait(Sh::B_SCF + (g & 3), (g >> 2) & 1));
-                ok = ok && all(wait(Sh::B_SF + t, n & 1));
-                if (!ok) break;
-                tc::fence_after_sync();
+                if (!(ok = all(wait(Sh::B_SCF + (g & 3), (g >> 2) & 1)))) break;
                 const int tile0 = 4 * (it.step0 + j);  // the step's first sub-tile
                 const float4* mt = meta + (g & 3) * 4;
                 const bool masked = (tile0 + 4) * TILE > it.s.base || mt[0].x + mt[1].x + mt[2].x + mt[3].x != 0.0f;
+                auto window = [&](int w) -> uint32_t {
+                    return row < rows ? node_window(P, it.s.q0, node, it.s.nb,
+                                                    (tile0 + w) * TILE - it.s.base)
+                                      : 0u;
+                };
+                // hi and lo parts: the row's windows, all loads in flight while S is made.  (Their
+                // four registers cost the bf16 forms, with less work a step, more than that:
+                // 128 rows 232 -> 268 us.)
+                uint32_t win[4] = {0u, 0u, 0u, 0u};
+                if (HILO && masked) {
+#pragma unroll
+                    for (int w = 0; w < 4; w++) win[w] = window(w);
+                }
+                if (!(ok = all(wait(Sh::B_SF + t, n & 1)))) break;
+                tc::fence_after_sync();
                 bool lost = false;  // the row sees a V step that is not finite
                 // columns 32 w .. + 31: x * f is the score (base 2), -inf where the row does not
                 // see the token; top bounds the exponents of the V steps that it sees
@@ -696,14 +710,14 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                         }
                     }
                     if (masked) {
-                        uint32_t win = 0u;
-                        if (row < rows)
-                            win = node_window(P, it.s.q0, node, it.s.nb, (tile0 + w) * TILE - it.s.base);
+                        const uint32_t on_w = !HILO ? window(w)
+                                              : w < 2 ? (w == 0 ? win[0] : win[1])
+                                                      : (w == 2 ? win[2] : win[3]);
                         float most = -90.0f;
 #pragma unroll
                         for (int c = 0; c < 32; c++) {
                             const float l = km[256 + 32 * w + c];
-                            const bool on = ((win >> krow(tc_rho(c))) & 1u) && l > -INFINITY;
+                            const bool on = ((on_w >> krow(tc_rho(c))) & 1u) && l > -INFINITY;
                             lost |= on && l == INFINITY;
                             if (on && l < INFINITY) most = fmaxf(most, l);
                             x[c] = on ? x[c] : -INFINITY;
