@@ -32,6 +32,11 @@
 // What bounds it: 16 MMAs of 128 x 128 x 16 per tile and block, 8192 FLOP per cycle and
 // SM at best (64 cycles each, measured), against 16384 exponentials per tile in the
 // same time (4 cycles a warp and sub-partition, measured).
+// Measured, bf16: four prompts of 1000 to 8192 tokens, 32/8 heads, 870 us = 1.34 PFLOP/s
+// (0.68 of a library GEMM's burst rate; the tensor pipe is active in 65 % of an SM's
+// cycles, the rest is the hand-over between softmax and MMA threads and a CTA's first and
+// last block); 4059 tokens, 16/8 heads, 56 us: 256 CTAs of 1 to 32 blocks on 152 SMs,
+// longest first; 506 tokens 12 us, four blocks one after the other.
 #include <cstdint>
 #include <cstring>
 

@@ -349,6 +349,7 @@ __global__ void __launch_bounds__(RW_THREADS) kq8_read_kernel(const RowsParams P
 // 0-7 K, 8-15 V, a 16-byte (q4: 8-byte) piece each.
 // A path with a bad entry, position or page moves nothing and sets a status
 // bit; every block of the sequence checks the whole path, so all agree.
+// A launch's latency bounds it (a path has a few rows, 264 bytes each and head).
 // ---------------------------------------------------------------------------
 constexpr int CM_THREADS = 256;
 constexpr int CM_ROWS = CM_THREADS / 16;
