@@ -421,3 +421,44 @@ def test_out_over_q_is_refused():
     c.out = c.q
     with pytest.raises(kq8.Kq8Error):
         c.run()
+
+
+@pytest.mark.parametrize("nodes,dtype", [(4, torch.bfloat16), (20, torch.bfloat16), (20, torch.float32)])
+def test_pages_past_2_gib(nodes, dtype):
+    """The same tokens in the first pages of a pool and in its last ones, past 2^31 bytes of
+    K and of V: the same outputs bit for bit."""
+    nq, nkv, kv_bs, n = 32, 8, 256, 600
+    pages = (1 << 31) // (kv_bs * nkv * 128) + 8
+    cache = kq8.PagedKVCache(pages, nkv, kv_bs, DEV)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(6)
+    k, v = (torch.randn((n, nkv, 128), generator=g, device=DEV) for _ in range(2))
+    q = torch.randn((nodes, nq, 128), generator=g, device=DEV).to(dtype)
+    outs = []
+    for first in (0, pages - 3):
+        at = torch.arange(n, dtype=torch.int32, device=DEV)
+        kq8.kq8_write_kv(cache, k, v, at + first * kv_bs)
+        out = torch.zeros_like(q)
+        ws = kq8.new_workspace(kq8.kq8_tree_workspace_bytes(1, nq, nkv, n, nodes), DEV)
+        kq8.kq8_tree_attn(out, q, cache, _ints([[first, first + 1, first + 2]]), _ints([n]),
+                          _ints([0, nodes]), None, n, nodes, SCALE, ws)
+        assert kq8.kq8_read_status(ws) == 0
+        outs.append(out)
+    assert torch.equal(outs[0], outs[1]) and bool((outs[0] != 0).any())
+
+
+@pytest.mark.parametrize("seed", range(8))
+def test_random_shapes(seed):
+    r = np.random.default_rng(1000 + seed)
+    for _ in range(4):
+        nkv, G, B = int(r.choice([1, 2, 3, 8])), int(r.integers(1, 9)), int(r.integers(1, 6))
+        lens = [int(2 ** r.uniform(0, 11)) for _ in range(B)]
+        most = int(r.choice([3, 9, 33, 70, 200]))
+        nodes = [int(r.integers(0, min(n, most) + 1)) for n in lens]
+        nodes[0] = max(nodes[0], 1)
+        c = Case(G * nkv, nkv, lens, nodes, [torch.float32, torch.bfloat16, torch.float16][seed % 3],
+                 kv_bs=int(r.choice([32, 64, 128, 256])), seed=int(r.integers(1 << 20)),
+                 layout=str(r.choice(["fused", "heads", "packed"])), extra_rows=int(r.integers(3)))
+        mask = bool(r.random() < 0.75)
+        assert c.run(mask=mask) == 0
+        c.check(*c.reference(mask=mask))
