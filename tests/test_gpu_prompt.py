@@ -184,3 +184,17 @@ def test_streams_and_graph():
             g.replay()
     torch.cuda.synchronize()
     assert torch.equal(outs[0], want)
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_random_shapes(seed):
+    r = np.random.default_rng(2000 + seed)
+    for _ in range(6):
+        nkv, G = int(r.choice([1, 2, 3])), int(r.integers(1, 9))
+        lens = [int(2 ** r.uniform(-1, 10.5)) for _ in range(int(r.integers(1, 7)))]
+        lens[0] = max(lens[0], 1)
+        first, behind = int(r.integers(4)), int(r.integers(4))
+        cu = (first + np.concatenate([[0], np.cumsum(lens)])).tolist()
+        q, k, v = _inputs(cu[-1] + behind, G * nkv, nkv, [torch.bfloat16, torch.float16][seed % 2],
+                          str(r.choice(["fused", "heads", "packed"])), seed=int(r.integers(1 << 20)))
+        _check(_run(q, k, v, cu, max(lens) + int(r.integers(200))), q, k, v, cu)
