@@ -12,7 +12,7 @@
 //
 // Work decomposition: CTA = (KV chunk, tile of 16 or 32 rows, KV head, sequence), 4
 // warps.  The rows of a KV head are its G query heads of every node.  As in the
-// decode kernel each warp owns a two-stage ring of 32-token sub-tiles filled by
+// decode kernel each warp owns a ring (two or three stages) of 32-token sub-tiles filled by
 // bulk and tensor copies, and takes every fourth sub-tile of its chunk; chunks
 // are merged by the last CTA to finish (a ticket).  Per sub-tile, on the warp's
 // matrix instructions (m16n8k16, fp16 in, fp32 out):

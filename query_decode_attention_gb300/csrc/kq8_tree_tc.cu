@@ -82,8 +82,10 @@ struct TcShape {
     static_assert(T == 1 || !HILO, "hi and lo parts of one tile");
     static constexpr int NR = 128 * T;                 // rows of a list
     // Rings, as far as shared memory goes.  A parity wait is only sound for a waiter
-    // that waits for every phase of a barrier, in order: so the raw ring is a multiple
-    // of four long (a place has the same two consumers, sub-tile w's K and V warp).
+    // that waits for every phase of a barrier, in order, or knows the phase before to be
+    // over (the softmax, which waits for PV at a list's end only: S of that step had
+    // waited for the step before's).  So the raw ring is a multiple of four long (a place
+    // has the same two consumers, sub-tile w's K and V warp).
     // One tile and one part leave room for a second place of K or of V; V's it is:
     // 128 rows of 16 x 16384 tokens took 268 us so, 292 with K's.  Raw places given up
     // for either cost more than it gains.
