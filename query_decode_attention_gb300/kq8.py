@@ -539,16 +539,18 @@ def _where(name: str, device: int, t: torch.Tensor, dtype=torch.int32) -> int:
     return t.data_ptr()
 
 
-def _rows(name: str, device: int, t: torch.Tensor, dtype) -> int:
-    """Pointer of a [tokens, heads, 128] tensor whose rows are adjacent elements."""
+def _rows(name: str, device: int, t: torch.Tensor, dtype):
+    """Pointer, shape and strides of a [tokens, heads, 128] tensor whose rows are adjacent
+    elements."""
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.get_device() != device:
         raise ValueError("kq8 takes CUDA tensors of one device" if t.is_cuda
                          else "kq8 takes CUDA tensors")
-    if t.dim() != 3 or t.shape[2] != HEAD_DIM or t.stride(2) != 1:
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 3 or shape[2] != HEAD_DIM or strides[2] != 1:
         raise ValueError(f"{name} must be [tokens, heads, 128] with adjacent elements in a row")
-    return t.data_ptr()
+    return t.data_ptr(), shape, strides
 
 
 def _launch_on(device: int, stream) -> int:
@@ -574,13 +576,12 @@ def _rows_args(cache, k, v, slot, status, stream):
     dev, dt = cache.k.get_device(), k.dtype
     code = _type_code("k", k)
     st = _launch_on(dev, stream)
-    kp, vp = _rows("k", dev, k, dt), _rows("v", dev, v, dt)
+    kp, shape, (kt, kh, _) = _rows("k", dev, k, dt)
+    vp, vshape, (vt, vh, _) = _rows("v", dev, v, dt)
     sp, T = _where("slot", dev, slot), slot.numel()
-    if k.shape != v.shape or k.shape[0] != T or k.shape[1] != cache.num_kv_heads:
+    if shape != vshape or shape[0] != T or shape[1] != cache.num_kv_heads:
         raise ValueError("k and v must be [len(slot), nkv, 128]")
     wp = None if status is None else _where("status", dev, status)
-    kt, kh, _ = k.stride()
-    vt, vh, _ = v.stride()
     return cache.ref, cache.bits, kp, vp, code, kt, kh, vt, vh, sp, T, wp, st
 
 
@@ -621,14 +622,14 @@ def kq8_tree_attn(out: torch.Tensor, q: torch.Tensor, cache: PagedKVCache,
     dev, dt = cache.k.get_device(), q.dtype
     code = _type_code("q", q)
     st = _launch_on(dev, stream)
-    qp, op = _rows("q", dev, q, dt), _where("out", dev, out, dt)
+    (qp, shape, (qt, qh, _)), op = _rows("q", dev, q, dt), _where("out", dev, out, dt)
     tp, lp = _where("page_table", dev, page_table), _where("seq_lens", dev, seq_lens)
     fp = _where("q_offsets", dev, q_offsets)
-    total, nq, _ = q.shape
-    B = seq_lens.numel()
-    if out.shape != q.shape:
+    total, nq, _ = shape
+    B, table = seq_lens.numel(), page_table.shape
+    if out.shape != shape:
         raise ValueError("q and out must be [total_q, nq, 128]")
-    if q_offsets.numel() != B + 1 or page_table.dim() != 2 or page_table.shape[0] != B:
+    if q_offsets.numel() != B + 1 or len(table) != 2 or table[0] != B:
         raise ValueError("q_offsets must be [B+1] and page_table [B, max_pages]")
     mp, words = None, 0
     if tree_mask is not None:
@@ -636,8 +637,7 @@ def kq8_tree_attn(out: torch.Tensor, q: torch.Tensor, cache: PagedKVCache,
         if tree_mask.dim() != 2 or tree_mask.shape[0] != total:
             raise ValueError("tree_mask must be [total_q, mask_words]")
         words = tree_mask.shape[1]
-    qt, qh, _ = q.stride()
-    rc = _lib.kq8_tree_attn(op, qp, code, qt, qh, total, cache.ref, tp, page_table.shape[1], lp, fp,
+    rc = _lib.kq8_tree_attn(op, qp, code, qt, qh, total, cache.ref, tp, table[1], lp, fp,
                             mp, words, int(max_seq_len), int(max_q_len), B, nq, float(scale),
                             _where("workspace", dev, workspace, workspace.dtype),
                             workspace.numel() * workspace.element_size(), st)
@@ -675,20 +675,19 @@ def kq8_prompt_attn(out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torc
     dev, dt = q.get_device(), q.dtype
     code = _type_code("q", q)
     st = _launch_on(dev, stream)
-    op, qp = _where("out", dev, out, dt), _rows("q", dev, q, dt)
-    kp, vp = _rows("k", dev, k, dt), _rows("v", dev, v, dt)
+    op = _where("out", dev, out, dt)
+    qp, shape, (qt, qh, _) = _rows("q", dev, q, dt)
+    kp, kshape, (kt, kh, _) = _rows("k", dev, k, dt)
+    vp, vshape, (vt, vh, _) = _rows("v", dev, v, dt)
     cp, B = _where("cu_seqlens", dev, cu_seqlens), cu_seqlens.numel() - 1
-    if out.shape != q.shape or k.shape != v.shape or k.shape[0] != q.shape[0]:
+    if out.shape != shape or kshape != vshape or kshape[0] != shape[0]:
         raise ValueError("q and out must be [total, nq, 128], k and v [total, nkv, 128]")
     if B < 0 or cu_seqlens.dim() != 1:
         raise ValueError("cu_seqlens must be [B+1]")
     wp = None if status is None else _where("status", dev, status)
-    qt, qh, _ = q.stride()
-    kt, kh, _ = k.stride()
-    vt, vh, _ = v.stride()
-    total, nq, _ = q.shape
+    total, nq, _ = shape
     rc = _lib.kq8_prompt_attn(op, qp, kp, vp, code, qt, qh, kt, kh, vt, vh, cp, total,
-                              int(max_len), B, nq, k.shape[1], float(scale), wp, st)
+                              int(max_len), B, nq, kshape[1], float(scale), wp, st)
     if rc:
         raise Kq8Error(rc, "kq8_prompt_attn")
 
